@@ -1,7 +1,7 @@
 """B200 (sm_100a) SVDQuant W4A4 linear layer -- Python binding of the C ABI.
 
-The entry points mirror include/svdq.h name for name and only marshal
-arguments (pointers, sizes, streams); all arithmetic runs in the CUDA library
+The entry points mirror include/svdq.h (and, in attention.py, include/svdq_attn.h)
+name for name and only marshal arguments (pointers, sizes, streams); all arithmetic runs in the CUDA library
 ``_lib/libsvdq_b200.so`` (build it with ``python -m bit_quantized_linear_svdq_b200.build``).
 There is no fallback: if the library is missing or cannot be loaded, every
 call raises.
@@ -27,6 +27,9 @@ __all__ = [
     "hadamard_transform", "SVDQLinear", "STATUS", "svdq_mxfp4_desc", "svdq_mxfp4_create", "svdq_mxfp4_destroy",
     "svdq_mxfp4_workspace_bytes", "svdq_mxfp4_quantize", "svdq_mxfp4_forward", "svdq_mxfp4_device_status",
     "mxfp4_quantize", "MXFP4Linear", "svdq_fp4_mma_loop", "svdq_fp4_mma_loop_status",
+    "qk_norm_rope", "rope_frequencies", "KV4Cache", "kv4_cache", "kv4_append", "kv4_read", "kv4_attention",
+    "svdq_heads", "svdq_qk_norm_rope_desc", "svdq_kv4_cache", "svdq_kv4_attention_desc", "svdq_qk_norm_rope",
+    "svdq_kv4_append", "svdq_kv4_read", "svdq_kv4_attention_workspace_bytes", "svdq_kv4_attention",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -111,6 +114,12 @@ def load_library() -> ctypes.CDLL:
         "svdq_mxfp4_device_status": (ci, [vp, ctypes.POINTER(ci)]),
         "svdq_fp4_mma_loop": (ci, [ci, ctypes.POINTER(ci), vp]),
         "svdq_fp4_mma_loop_status": (ci, [ctypes.POINTER(ci)]),
+        # include/svdq_attn.h (attention.py): descriptions are passed by address.
+        "svdq_qk_norm_rope": (ci, [vp, vp]),
+        "svdq_kv4_append": (ci, [vp, vp, vp, ci, ci, vp, vp]),
+        "svdq_kv4_read": (ci, [vp, vp, vp, ci, ci, vp, vp]),
+        "svdq_kv4_attention_workspace_bytes": (cs, [vp]),
+        "svdq_kv4_attention": (ci, [vp, vp, cs, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -459,3 +468,9 @@ class SVDQLinear:
             self.close()
         except Exception:
             pass
+
+
+from .attention import (KV4Cache, kv4_append, kv4_attention, kv4_cache, kv4_read, qk_norm_rope,  # noqa: E402
+                        rope_frequencies, svdq_heads, svdq_kv4_append, svdq_kv4_attention,
+                        svdq_kv4_attention_desc, svdq_kv4_attention_workspace_bytes, svdq_kv4_cache,
+                        svdq_kv4_read, svdq_qk_norm_rope, svdq_qk_norm_rope_desc)

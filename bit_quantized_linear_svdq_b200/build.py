@@ -4,7 +4,8 @@ Usage:  python -m bit_quantized_linear_svdq_b200.build [--verbose]
 
 Compiles every csrc/*.cu with nvcc for sm_100a only (the kernels use tcgen05,
 TMA and the FP4 converts, which exist on that target alone) and links one
-shared library exporting the C ABI declared in include/svdq.h.
+shared library exporting the C ABI declared in include/svdq.h and
+include/svdq_attn.h.
 """
 from __future__ import annotations
 
@@ -39,7 +40,7 @@ def _nvcc() -> str:
 def _sources():
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = srcs + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")))
-    deps.append(os.path.join(ROOT, "include", "svdq.h"))
+    deps += sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
     return srcs, deps
 
 

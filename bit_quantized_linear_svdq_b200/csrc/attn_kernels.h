@@ -1,0 +1,74 @@
+// attn_kernels.h -- host-side launch interface of the attention-side kernels
+// (internal to the library; the public boundary is include/svdq_attn.h).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace svdq {
+
+// Text returned by svdq_last_error on this thread (never throws).
+void set_last_error(const char* text) noexcept;
+
+// One side (queries or keys) of the head norm / rotary / Hadamard pass.
+struct HeadSide {
+  const void* x;
+  void* y;
+  const void* weight;             // (D) in the storage type, or null: no norm
+  long long xt, xh, yt, yh;       // token and head strides in elements
+  int heads;
+};
+struct QkNormRopeLaunch {
+  HeadSide q, k;
+  const int* positions;           // (tokens, axes), row stride pos_stride
+  const float* inv_freq;          // (pairs)
+  const uint8_t* pair_axis;       // (pairs) or null: axis 0
+  long long pos_stride;
+  int tokens, D, dtype, axes, pairs;
+  float eps;
+  bool interleaved, hadamard;
+};
+cudaError_t launch_qk_norm_rope(const QkNormRopeLaunch& p, cudaStream_t stream);
+
+
+// The 4-bit key/value cache: codes (pages, heads, page, D/2), e4m3 scales
+// (pages, heads, page, D/16), D = 64 or 128, page = 1 << page_log2 >= 16.
+struct Kv4Cache {
+  uint8_t *kc, *ks, *vc, *vs;
+  long long pages;
+  int heads, D, page_log2;
+};
+struct Kv4RowsLaunch {
+  Kv4Cache c;
+  const void *k, *v;              // append: inputs
+  void *k_out, *v_out;            // read: outputs
+  long long kt, kh, vt, vh;       // token and head strides of k / v (or k_out / v_out), elements
+  const long long* slots;         // (tokens); page * page_size + offset, outside the cache: skipped / zeros
+  int tokens, dtype;
+};
+cudaError_t launch_kv4_append(const Kv4RowsLaunch& p, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Kv4RowsLaunch& p, cudaStream_t stream);
+
+struct Kv4AttnLaunch {
+  Kv4Cache c;
+  const void* q;
+  void* out;
+  float* lse;                     // (tokens, q_heads) or null
+  long long qt, qh, ot, oh;       // token and head strides, elements
+  const int* kv_len;              // (requests)
+  const int* q_start;             // (requests + 1) or null: tokens / requests each
+  const int* table;               // (requests, max_pages), row stride table_stride
+  long long table_stride;
+  int max_pages, requests, tokens, q_heads, dtype, causal;
+  float scale;                    // softmax scale
+  int splits, chunk;              // key axis: `splits` parts of `chunk` keys, the last to the end
+  float* part_o;                  // splits > 1: (splits, tokens, q_heads, D) fp32
+  float2* part_ml;                //             (splits, tokens, q_heads) {max, sum} in base 2
+};
+// Fills splits and chunk for `max_kv` keys a request; the launch needs
+// kv4_attention_workspace bytes for part_o / part_ml then.
+void kv4_attention_plan(Kv4AttnLaunch& p, int max_kv);
+size_t kv4_attention_workspace(const Kv4AttnLaunch& p);
+cudaError_t launch_kv4_attention(const Kv4AttnLaunch& p, void* workspace, cudaStream_t stream);
+
+}  // namespace svdq

@@ -12,6 +12,7 @@
 #include <string>
 
 #include "svdq.h"
+#include "attn_kernels.h"
 #include "kcommon.cuh"
 #include "svdq_kernels.h"
 
@@ -297,6 +298,13 @@ WsLayout ws_layout(const svdq_linear* h, int M) {
 }
 
 }  // namespace
+
+void svdq::set_last_error(const char* text) noexcept {
+  try {
+    g_last_error = text;
+  } catch (...) {
+  }
+}
 
 extern "C" {
 
