@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -20,6 +21,25 @@ svdq_status fail(svdq_status s, const char* why) {
 svdq_status launched(cudaError_t e) { return e == cudaSuccess ? SVDQ_OK : fail(SVDQ_ERR_CUDA, cudaGetErrorString(e)); }
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// SMs of the current device, looked up once per device (a B200's count where
+// there is no device to ask: argument errors are answered without one).
+int num_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 148;
+  }
+  int n = dev >= 0 && dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return 148;
+  }
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
 
 // A tensor of heads with anything to read or write.
 svdq_status check_heads(const svdq_heads& h) {
@@ -38,6 +58,8 @@ svdq_status check_cache(const svdq_kv4_cache* c, svdq::Kv4Cache* out) {
   if ((1 << log2) != c->page_size) return fail(SVDQ_ERR_SHAPE, "page_size has to be 16, 32, 64, 128 or 256");
   if (c->heads < 1 || c->heads > 65535) return fail(SVDQ_ERR_SHAPE, "heads of the cache out of range");
   if (c->pages < 1 || c->pages > (1ll << 31)) return fail(SVDQ_ERR_SHAPE, "pages of the cache out of range");
+  // Rows (page, head, offset) are numbered in 32 bits: 2^32 rows are more than any device holds.
+  if (((c->pages * c->heads) << log2) >= 0xFFFFFFFFll) return fail(SVDQ_ERR_SHAPE, "the cache has too many rows");
   const void* ptr[4] = {c->k_codes, c->k_scales, c->v_codes, c->v_scales};
   for (const void* p : ptr)
     if (!p || !aligned(p, 16)) return fail(SVDQ_ERR_INVALID_ARG, "cache tensor null or not 16-byte aligned");
@@ -103,14 +125,18 @@ svdq_status check_attention(const svdq_kv4_attention_desc* d, svdq::Kv4AttnLaunc
   p->dtype = d->dtype;
   p->causal = d->causal != 0;
   p->scale = d->softmax_scale;
-  p->splits = 1;
-  p->chunk = 1;
+  p->num_sms = 0;
+  p->tile_rows = 8;
+  p->max_rows = 0;
+  p->segments = 0;
+  p->ctas = 1;
+  p->join = 0;
   p->part_o = nullptr;
   p->part_ml = nullptr;
   if (d->tokens > 0 && d->requests > 0) {
     const long long cap = (long long)d->max_pages << p->c.page_log2;
     const long long bound = d->max_kv_len > 0 && d->max_kv_len < cap ? d->max_kv_len : cap;
-    svdq::kv4_attention_plan(*p, (int)bound);
+    svdq::kv4_attention_plan(*p, (int)bound, num_sms());
   }
   return SVDQ_OK;
 }

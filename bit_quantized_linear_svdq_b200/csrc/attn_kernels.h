@@ -61,13 +61,17 @@ struct Kv4AttnLaunch {
   long long table_stride;
   int max_pages, requests, tokens, q_heads, dtype, causal;
   float scale;                    // softmax scale
-  int splits, chunk;              // key axis: `splits` parts of `chunk` keys, the last to the end
-  float* part_o;                  // splits > 1: (splits, tokens, q_heads, D) fp32
-  float2* part_ml;                //             (splits, tokens, q_heads) {max, sum} in base 2
+  // Set by kv4_attention_plan:
+  int num_sms;
+  int tile_rows, max_rows;        // rows of a tile (8, 16, 32); requests with more rows are left out
+  long long segments;             // tiles x heads, at most
+  int ctas, join;                 // CTAs that share the work; whether segments may be cut
+  float* part_o;                  // join: (ctas, 2, tile_rows, D) fp32
+  float2* part_ml;                //       (ctas, 2, tile_rows) {max, sum} in base 2
 };
-// Fills splits and chunk for `max_kv` keys a request; the launch needs
-// kv4_attention_workspace bytes for part_o / part_ml then.
-void kv4_attention_plan(Kv4AttnLaunch& p, int max_kv);
+// `max_kv`: keys a request has at most (for the number of CTAs only).  The
+// launch needs kv4_attention_workspace bytes, 16-byte aligned.
+void kv4_attention_plan(Kv4AttnLaunch& p, int max_kv, int num_sms);
 size_t kv4_attention_workspace(const Kv4AttnLaunch& p);
 cudaError_t launch_kv4_attention(const Kv4AttnLaunch& p, void* workspace, cudaStream_t stream);
 

@@ -8,9 +8,11 @@
 // a query that sees no key gets o = 0 and lse = -inf.
 //
 // Work split.  The query heads that share a key head, times the request's
-// tokens, are the rows of one tile (16 or 32); a CTA takes one tile, one key
-// head and one part of the key axis, its four warps alternate 16-key tiles and
-// join once at the end.  With several parts a second kernel joins them in
+// tokens, are the rows of one tile (16 or 32).  One resident set of CTAs takes
+// equal shares of all keys of all tiles and heads (kv4_rows.cuh), so unequal
+// lengths and counts that do not divide leave no SM idle; a share starts and
+// ends wherever it falls.  A CTA's four warps alternate 32-key tiles and join
+// once per tile; what a share's end cuts is joined by a second kernel, in
 // order (no atomics: results do not depend on timing).
 //
 // Arithmetic.  Both products run on fp16 tensor-core MMAs (m16n8k16) with fp32
@@ -21,13 +23,16 @@
 // row's largest value.  The softmax (base 2) is fp32; its weights, in [0, 1], are
 // rounded to fp16 (2^-11 relative) for the second product only.
 //
-// Layout.  The MMA's contraction and column indexes are free to permute, and
-// are chosen so that no dequantized value moves between lanes: lane (g, t) of
-// the first product takes 1/4 of key row g's codes (16 bytes for D = 128, one
-// shared-memory load), lane (g, t) of the second takes 1/8 of four keys' rows,
-// the same four keys t, 4+t, 8+t, 12+t whose scores it holds; two keys' codes
-// are interleaved as nibbles (two logic ops per 8 values) so that one convert
-// gives the pair of rows an MMA operand wants.
+// Layout.  Both products are transposed, keys (dims) on the MMA's 16 rows and
+// query rows on its 8 columns: at one to eight query rows a key head, the usual
+// case of decoding, nothing of the MMA or the softmax is wasted.  The
+// contraction and row indexes are free to permute, and are chosen so that no
+// dequantized value moves between lanes: lane (g, t) of the first product takes
+// a quarter of two key rows (16 bytes each for D = 128, one shared-memory
+// load), lane (g, t) of the second an eighth of the rows of keys t, 4+t, 8+t,
+// 12+t; two keys' codes are interleaved as nibbles (two logic ops per 8 values)
+// so that one convert gives the pair of keys an MMA operand wants.  Only the
+// weights change lanes (an 8x8 transpose, movmatrix).
 //
 // Bound: codes and scales are 9/16 byte a value, read once (HBM) with a ring of
 // cp.async copies per warp (no barrier between warps); dequantizing costs
@@ -48,7 +53,10 @@
 namespace svdq {
 namespace {
 
-constexpr int kWarpsA = 4, kThreadsA = 32 * kWarpsA, kTileA = 16, kStagesA = 4;
+constexpr int kWarpsA = 4, kThreadsA = 32 * kWarpsA, kTileA = 32, kStagesA = 2;
+constexpr uint32_t kAbsent = 0xFFFFFFFFu;             // no such row: past the keys, or in no page of the cache
+// Resident CTAs an SM by rows of a tile / 8: what the accumulators leave room for.
+__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -63,6 +71,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transposes an 8x8 matrix of 16-bit values held row-wise by the warp.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 __device__ __forceinline__ uint32_t hmul2u(uint32_t a, __half2 b) {
   const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
@@ -98,69 +112,80 @@ __device__ __forceinline__ void store_row8(const Kv4AttnLaunch& p, long long tok
 
 template <int D>
 struct Tile {
-  static constexpr int kCode = kTileA * D / 2, kScale = kTileA * D / 16;      // bytes of 16 keys
+  static constexpr int kCode = kTileA * D / 2, kScale = kTileA * D / 16;      // bytes of 32 keys
   static constexpr int kStage = 2 * kCode + 2 * kScale;
 };
-template <int D, int MT>
+template <int D, int NT>
 constexpr int smem_bytes() {
   const int ring = kWarpsA * kStagesA * Tile<D>::kStage;
-  const int join = kWarpsA * 16 * MT * (D + 4) * 4 + kWarpsA * 16 * MT * 8;
-  return ring > join ? ring : join;
+  const int join = kWarpsA * 8 * NT * (D + 4) * 4 + kWarpsA * 8 * NT * 8;
+  return (ring > join ? ring : join) + NT * (D / 32) * 512 + 8 * NT * 4;
 }
 
-// D: head dimension (64, 128).  MT: 16-row tiles per warp.  BF16: storage type of q and out.
-template <int D, int MT, bool BF16>
-__global__ void __launch_bounds__(kThreadsA, MT == 1 ? 3 : 2)
-    kv4_attention_kernel(const __grid_constant__ Kv4AttnLaunch p) {
-  constexpr int kRows = 16 * MT, kKS = D / 16, kDG = D / 8;       // MMA k-steps; head dims per lane group g
+// Keys [k_begin, k_end) of one segment: its rows' unnormalized outputs, maxima
+// and sums, joined over the CTA's warps, finished (whole) or left as a part.
+// D: head dimension (64, 128).  NT: 8-row tiles.  BF16: storage type of q and out.
+template <int D, int NT, bool BF16>
+__device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const RowTile& rt, int kvh, int k_begin, int k_end,
+                                               bool whole, long long part) {
+  constexpr int kRows = 8 * NT, kDM = D / 16;                     // rows of the tile; 16-dim tiles of the output
   constexpr int kCode = Tile<D>::kCode, kScale = Tile<D>::kScale, kStage = Tile<D>::kStage;
   extern __shared__ __align__(16) uint8_t smem[];
-
   const int group = p.q_heads / p.c.heads;
-  const RowTile rt = find_row_tile(p.q_start, p.kv_len, p.requests, p.tokens, group, kRows, blockIdx.x,
-                                   (long long)p.max_pages << p.c.page_log2, p.causal);
-  if (rt.rows <= 0) return;
-  const int active = active_parts(rt.last_key, p.splits, p.chunk);
-  const int part = blockIdx.y;
-  if (part >= active) return;
-  const int k_begin = part * p.chunk, k_end = part == active - 1 ? rt.last_key : k_begin + p.chunk;
-  const int kvh = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
-  // ---- ring: stage s of this warp holds one 16-key tile {K codes, V codes, K scales, V scales}
+  // ---- ring: stage s of this warp holds one 32-key tile {K codes, V codes, K scales, V scales}
   const uint32_t ring = smem_u32(smem) + warp * (kStagesA * kStage);
   const int n_tiles = (k_end - k_begin + kTileA - 1) / kTileA;
   const int my_tiles = n_tiles > warp ? (n_tiles - warp + kWarpsA - 1) / kWarpsA : 0;
   const int* table = p.table + rt.request * p.table_stride;
-  int page_ids = -1;                                      // lane i: page of this warp's tile (base + i)
-  uint32_t absent = 0;                                    // bit it % 32: tile it lies in no page of the cache
+  uint32_t rows16 = kAbsent;                              // lane i: cache row of 16-key half i & 1 of tile base + i / 2
+  uint32_t absent = 0;                                    // bits 2 (it % 16) + u: half u of tile it is in no page
   auto issue = [&](int it) {
-    if ((it & 31) == 0) {
-      const int k = k_begin + kTileA * (warp + kWarpsA * (it + lane));
-      page_ids = it + lane < my_tiles ? table[k >> p.c.page_log2] : -1;
-    }
-    const int page = __shfl_sync(0xFFFFFFFFu, page_ids, it & 31);
-    if (it < my_tiles) {
-      const int k0 = k_begin + kTileA * (warp + kWarpsA * it);
-      const bool ok = page >= 0 && page < p.c.pages;
-      absent = (absent & ~(1u << (it & 31))) | ((ok ? 0u : 1u) << (it & 31));
-      const int nv = ok ? min(kTileA, k_end - k0) : 0;    // keys of the tile that exist
-      const long long row = ((((long long)(ok ? page : 0)) * p.c.heads + kvh) << p.c.page_log2) +
-                            (k0 & ((1 << p.c.page_log2) - 1));
-      const uint32_t dst = ring + (it % kStagesA) * kStage;
-      constexpr int kChunks = kCode / 16, kPerKey = D / 32;           // 16-byte pieces: of a tile, of a key
-#pragma unroll
-      for (int i = 0; i < kChunks / 32; ++i) {
-        const int c = lane + 32 * i;
-        const int bytes = c / kPerKey < nv ? 16 : 0;
-        cp_async16(dst + 16 * c, p.c.kc + row * (D / 2) + 16 * c, bytes);
-        cp_async16(dst + kCode + 16 * c, p.c.vc + row * (D / 2) + 16 * c, bytes);
+    if ((it & 15) == 0) {
+      const int k = k_begin + kTileA * (warp + kWarpsA * (it + (lane >> 1))) + 16 * (lane & 1);
+      rows16 = kAbsent;
+      if (it + (lane >> 1) < my_tiles && k < k_end) {
+        const int page = table[k >> p.c.page_log2];
+        if (page >= 0 && page < p.c.pages)
+          rows16 = ((((uint32_t)page * p.c.heads) + kvh) << p.c.page_log2) + (k & ((1 << p.c.page_log2) - 1));
       }
-      constexpr int kSc = kScale / 16;                                // 16-byte pieces of one tensor's scales
-      if (lane < 2 * kSc) {
-        const int c = lane % kSc;
-        const uint8_t* src = (lane < kSc ? p.c.ks : p.c.vs) + row * (D / 16) + 16 * c;
-        cp_async16(dst + 2 * kCode + 16 * lane, src, max(0, min(16, nv * (D / 16) - 16 * c)));
+    }
+    uint32_t row[2];
+    row[0] = __shfl_sync(0xFFFFFFFFu, rows16, 2 * (it & 15));
+    row[1] = __shfl_sync(0xFFFFFFFFu, rows16, 2 * (it & 15) + 1);
+    if (it < my_tiles) {
+      const int k0 = k_begin + kTileA * (warp + kWarpsA * it), sh = 2 * (it & 15);
+      absent = (absent & ~(3u << sh)) | ((row[0] == kAbsent ? 1u : 0u) << sh) | ((row[1] == kAbsent ? 2u : 0u) << sh);
+      const uint32_t dst = ring + (it % kStagesA) * kStage + 16 * lane;
+      constexpr int kPerHalf = D / 64;                    // 16-byte pieces a lane of one half's codes
+      constexpr int kSc = D / 16;                         // 16-byte pieces of one half's scales
+      const int tensor = lane / (2 * kSc), su = lane / kSc & 1, sp = lane % kSc;
+      const uint8_t* scales = (tensor ? p.c.vs : p.c.ks) + 16 * sp;
+      if (row[0] != kAbsent && row[1] != kAbsent && k0 + kTileA <= k_end) {
+#pragma unroll
+        for (int i = 0; i < 2 * kPerHalf; ++i) {
+          const size_t at = (size_t)row[i / kPerHalf] * (D / 2) + 16 * (lane + 32 * (i % kPerHalf));
+          cp_async16(dst + 512 * i, p.c.kc + at, 16);
+          cp_async16(dst + kCode + 512 * i, p.c.vc + at, 16);
+        }
+        if (lane < 4 * kSc) cp_async16(dst + 2 * kCode, scales + (size_t)row[su] * (D / 16), 16);
+      } else {                                            // rows that do not exist become zeros
+        int nv[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          nv[u] = row[u] == kAbsent ? 0 : min(16, k_end - k0 - 16 * u);
+          if (row[u] == kAbsent) row[u] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * kPerHalf; ++i) {
+          const int c = lane + 32 * (i % kPerHalf), bytes = c / (D / 32) < nv[i / kPerHalf] ? 16 : 0;
+          const size_t at = (size_t)row[i / kPerHalf] * (D / 2) + 16 * c;
+          cp_async16(dst + 512 * i, p.c.kc + at, bytes);
+          cp_async16(dst + kCode + 512 * i, p.c.vc + at, bytes);
+        }
+        if (lane < 4 * kSc)
+          cp_async16(dst + 2 * kCode, scales + (size_t)row[su] * (D / 16), max(0, min(16, nv[su] * (D / 16) - 16 * sp)));
       }
     }
     cp_commit();
@@ -168,242 +193,279 @@ __global__ void __launch_bounds__(kThreadsA, MT == 1 ? 3 : 2)
 #pragma unroll
   for (int s = 0; s < kStagesA - 1; ++s) issue(s);
 
-  // ---- queries: rows g and g + 8 of each 16-row tile, this lane's quarter of the head
-  uint32_t qa[MT][kKS][4];
-  float qs[MT][2];                                        // row factor: scale * log2e / 2^shift
-  int lim[MT][2];                                         // keys the row sees
+  // ---- queries, as the first product's column operand: in shared memory, for every two MMA steps one 16-byte piece a
+  // lane.  Lane (g, t) prepares row g of an 8-row tile, a quarter of the head; warp w the tiles w, w + 4, ...
+  constexpr int kQ = smem_bytes<D, NT>() - NT * (D / 32) * 512 - kRows * 4;
+  uint4* qsm = reinterpret_cast<uint4*>(smem + kQ);                             // [NT][D / 32][32 lanes]
+  float* back = reinterpret_cast<float*>(smem + kQ + NT * (D / 32) * 512);      // [rows] scale * log2e / 2^shift
+  auto keys_of_row = [&](int r) {
+    return r < rt.rows ? rt.keys_of((rt.row0 + r) / group, p.causal) : 0;
+  };
+  for (int n = warp; n < NT; n += kWarpsA) {
+    const int r = 8 * n + g;
+    float f[D / 4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+    for (int i = 0; i < D / 4; ++i) f[i] = 0.0f;
+    if (r < rt.rows) {
+      const int row = rt.row0 + r, tok = row / group, head = kvh * group + row - tok * group;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                        (long long)(rt.token0 + tok) * p.qt + head * p.qh + t * (D / 4));
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int r = 16 * m + 8 * hf + g;
-      float f[D / 4];
-      lim[m][hf] = 0;
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 w = src[i];
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int i = 0; i < D / 4; ++i) f[i] = 0.0f;
-      if (r < rt.rows) {
-        const int row = rt.row0 + r, tok = row / group, head = kvh * group + row - tok * group;
-        lim[m][hf] = rt.keys_of(tok, p.causal);
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                          (long long)(rt.token0 + tok) * p.qt + head * p.qh + t * (D / 4));
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 w = src[i];
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (BF16) {
-              f[8 * i + 2 * j] = bf16lo_to_f32(x[j]);
-              f[8 * i + 2 * j + 1] = bf16hi_to_f32(x[j]);
-            } else {
-              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-              f[8 * i + 2 * j] = v.x;
-              f[8 * i + 2 * j + 1] = v.y;
-            }
+        for (int j = 0; j < 4; ++j) {
+          if (BF16) {
+            f[8 * i + 2 * j] = bf16lo_to_f32(x[j]);
+            f[8 * i + 2 * j + 1] = bf16hi_to_f32(x[j]);
+          } else {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+            f[8 * i + 2 * j] = v.x;
+            f[8 * i + 2 * j + 1] = v.y;
           }
         }
       }
-      // Power of two that takes the row's largest finite magnitude to [2^14, 2^15).
-      float mx = 0.0f;
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) mx = fmaxf(mx, fabsf(f[i]) < INFINITY ? fabsf(f[i]) : 0.0f);
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-      // Exponent clamped so that both 2^e and 2^-e are normal numbers.
-      const int e = mx > 0.0f ? min(max(14 - (int)((__float_as_uint(mx) >> 23) & 0xFF) + 127, -126), 126) : 0;
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      qs[m][hf] = p.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-      for (int j = 0; j < kKS; ++j) {
-        qa[m][j][hf] = half2u(f[4 * j] * up, f[4 * j + 1] * up);
-        qa[m][j][2 + hf] = half2u(f[4 * j + 2] * up, f[4 * j + 3] * up);
-      }
     }
+    // Power of two that takes the row's largest finite magnitude to [2^14, 2^15).
+    float big = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) big = fmaxf(big, fabsf(f[i]) < INFINITY ? fabsf(f[i]) : 0.0f);
+    big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+    // Exponent clamped so that both 2^e and 2^-e are normal numbers.
+    const int e = big > 0.0f ? min(max(14 - (int)((__float_as_uint(big) >> 23) & 0xFF) + 127, -126), 126) : 0;
+    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+    if (t == 0) back[r] = p.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      qsm[(n * (D / 32) + i) * 32 + lane] =
+          make_uint4(half2u(f[8 * i] * up, f[8 * i + 1] * up), half2u(f[8 * i + 2] * up, f[8 * i + 3] * up),
+                     half2u(f[8 * i + 4] * up, f[8 * i + 5] * up), half2u(f[8 * i + 6] * up, f[8 * i + 7] * up));
   }
+  __syncthreads();
+  float qs[NT][2];                                        // factor of rows 2t, 2t + 1
+  int lim[NT][2];                                         // keys that they see
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      qs[n][c] = back[8 * n + 2 * t + c];
+      lim[n][c] = keys_of_row(8 * n + 2 * t + c);
+    }
   // Tiles that end at or before the first row's keys need no mask.
   const int free_end = min(rt.keys_of(rt.row0 / group, p.causal), k_end);
 
-  float o[MT][kDG][4], mx[MT][2], sum[MT][2];
+  // Rows 2t, 2t + 1 of each tile: reference exponent (base 2), sum of weights, outputs.
+  float o[NT][kDM][4], ref[NT][2], sum[NT][2];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    mx[m][0] = mx[m][1] = -INFINITY;
-    sum[m][0] = sum[m][1] = 0.0f;
+  for (int n = 0; n < NT; ++n) {
+    ref[n][0] = ref[n][1] = -INFINITY;
+    sum[n][0] = sum[n][1] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kDG; ++i) o[m][i][0] = o[m][i][1] = o[m][i][2] = o[m][i][3] = 0.0f;
+    for (int i = 0; i < kDM; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
   }
 
   for (int it = 0; it < my_tiles; ++it) {
     issue(it + kStagesA - 1);
     cp_wait<kStagesA - 1>();
     __syncwarp();
-    if ((absent >> (it & 31)) & 1u) continue;
+    const uint32_t gone = (absent >> (2 * (it & 15))) & 3u;
+    if (gone == 3u) continue;
     const uint8_t* st = smem + warp * (kStagesA * kStage) + (it % kStagesA) * kStage;
     const int k0 = k_begin + kTileA * (warp + kWarpsA * it);
 
-    // ---- scores: column n of the MMA is key (n >> 1) + 4 (n & 1) of its 8-key half
-    float s[MT][2][4];
+    // ---- scores (keys x rows), one MMA row tile per 16-key half u: its row r is key (r >> 1) + 4 (r & 1) (+ 8 for r >= 8)
+    float s[2][NT][4];
+    uint32_t w[2][2][D / 32];
+    __half2 sc[2][2][2];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const int key = 8 * nt + (g >> 1) + 4 * (g & 1);
-      uint32_t w[D / 32];
-      __half2 sc[2];
-      if (D == 128) {
-        const uint4 c = *reinterpret_cast<const uint4*>(st + key * 64 + 16 * t);
-        w[0] = c.x, w[1] = c.y, w[2 % (D / 32)] = c.z, w[3 % (D / 32)] = c.w;
-        const __half2 two = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(st + 2 * kCode + key * 8 + 2 * t));
-        sc[0] = __low2half2(two);
-        sc[1] = __high2half2(two);
-      } else {
-        const uint2 c = *reinterpret_cast<const uint2*>(st + key * 32 + 8 * t);
-        w[0] = c.x, w[1] = c.y;
-        const uint32_t b = st[2 * kCode + key * 4 + t];
-        sc[0] = sc[1] = e4m3x2_to_half2(b | (b << 8));
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.0f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = 16 * u + (g >> 1) + 4 * (g & 1) + 8 * h;
+        if (D == 128) {
+          const uint4 c = *reinterpret_cast<const uint4*>(st + k * 64 + 16 * t);
+          w[u][h][0] = c.x, w[u][h][1] = c.y, w[u][h][2 % (D / 32)] = c.z, w[u][h][3 % (D / 32)] = c.w;
+          const __half2 two = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(st + 2 * kCode + k * 8 + 2 * t));
+          sc[u][h][0] = __low2half2(two);
+          sc[u][h][1] = __high2half2(two);
+        } else {
+          const uint2 c = *reinterpret_cast<const uint2*>(st + k * 32 + 8 * t);
+          w[u][h][0] = c.x, w[u][h][1] = c.y;
+          const uint32_t b = st[2 * kCode + k * 4 + t];
+          sc[u][h][0] = sc[u][h][1] = e4m3x2_to_half2(b | (b << 8));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint32_t a[2][2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t d[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          e2m1x8_to_f16x8(w[u][h][i], d[h]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[u][j >> 1][h + 2 * (j & 1)] = hmul2u(d[h][j], sc[u][h][i / 2]);
+        }
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m) s[m][nt][0] = s[m][nt][1] = s[m][nt][2] = s[m][nt][3] = 0.0f;
+      for (int n = 0; n < NT; ++n) {
+        const uint4 q = qsm[(n * (D / 32) + i) * 32 + lane];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t d[4];
-        e2m1x8_to_f16x8(w[i], d);
-        const __half2 f = sc[i / 2];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = hmul2u(d[j], f);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma16816(s[m][nt], qa[m][2 * i], d[0], d[1]);
-          mma16816(s[m][nt], qa[m][2 * i + 1], d[2], d[3]);
+        for (int u = 0; u < 2; ++u) {
+          mma16816(s[u][n], a[u][0], q.x, q.y);
+          mma16816(s[u][n], a[u][1], q.z, q.w);
         }
       }
     }
 
-    // ---- softmax weights of keys t, 4+t (nt 0) and 8+t, 12+t (nt 1)
-    const bool masked = k0 + kTileA > free_end;
-    uint32_t pa[MT][4];
-    bool grew = false;
-    float to[MT][2];
+    // ---- weights.  s[u][.][0..1]: key kg + 16u, rows 2t and 2t + 1; s[u][.][2..3]: key kg + 16u + 8.  The reference
+    // exponent is raised only when a score exceeds it by more than 2^8 (or at a row's first key): weights stay below 2^8.
+    const bool masked = gone != 0 || k0 + kTileA > free_end;
+    const int kg = k0 + (g >> 1) + 4 * (g & 1);
+    float x[2][NT][4];
+    auto exponents = [&]() {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float base = ref[n][c & 1] == -INFINITY ? 0.0f : ref[n][c & 1];
+            x[u][n][c] = fmaf(s[u][n][c], qs[n][c & 1], -base);
+          }
+      if (masked) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (((gone >> u) & 1u) || kg + 16 * u + 8 * (c >> 1) >= lim[n][c & 1]) x[u][n][c] = -INFINITY;
+      }
+    };
+    exponents();
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        over |= fmaxf(fmaxf(x[0][n][c], x[0][n][2 + c]), fmaxf(x[1][n][c], x[1][n][2 + c])) >
+                (ref[n][c] == -INFINITY ? -INFINITY : 8.0f);
+    if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float v = fmaxf(fmaxf(x[0][n][c], x[0][n][2 + c]), fmaxf(x[1][n][c], x[1][n][2 + c]));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+          const float to = ref[n][c] == -INFINITY ? v : ref[n][c] + fmaxf(v, 0.0f);
+          const float f = ex2_diff(ref[n][c], to);
+          ref[n][c] = to;
+          sum[n][c] *= f;
+#pragma unroll
+          for (int i = 0; i < kDM; ++i) {
+            o[n][i][c] *= f;
+            o[n][i][2 + c] *= f;
+          }
+        }
+      exponents();
+    }
+    uint32_t pb[2][NT][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          s[m][nt][c] *= qs[m][c >> 1];
-          if (masked && k0 + 8 * nt + t + 4 * (c & 1) >= lim[m][c >> 1]) s[m][nt][c] = -INFINITY;
+          x[u][n][c] = ex2(x[u][n][c]);
+          sum[n][c & 1] += x[u][n][c];
         }
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float v = fmaxf(fmaxf(s[m][0][2 * hf], s[m][0][2 * hf + 1]), fmaxf(s[m][1][2 * hf], s[m][1][2 * hf + 1]));
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-        to[m][hf] = fmaxf(mx[m][hf], v);
-        grew |= to[m][hf] > mx[m][hf];
+        // (key, rows 2t 2t+1) -> (keys 2t 2t+1, row g): the second product's operand.
+        pb[u][n][0] = movmatrix(half2u(x[u][n][0], x[u][n][1]));
+        pb[u][n][1] = movmatrix(half2u(x[u][n][2], x[u][n][3]));
       }
-    }
-    if (__any_sync(0xFFFFFFFFu, grew)) {
+
+    // ---- values (dims x keys): lane (g, t) takes D/8 dims from D/8 g on, of keys t, 4+t, 8+t, 12+t of each half
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* vs = st + 2 * kCode + kScale + u * (kScale / 2) + (D == 128 ? g : g >> 1);
+      uint32_t sb[4];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const float f = ex2_diff(mx[m][hf], to[m][hf]);
-          mx[m][hf] = to[m][hf];
-          sum[m][hf] *= f;
+      for (int c = 0; c < 4; ++c) sb[c] = vs[(t + 4 * c) * (D / 16)];
+      if (masked) {
+        bool bad = false;
 #pragma unroll
-          for (int i = 0; i < kDG; ++i) {
-            o[m][i][2 * hf] *= f;
-            o[m][i][2 * hf + 1] *= f;
+        for (int c = 0; c < 4; ++c) bad |= (sb[c] & 0x7Fu) == 0x7Fu;
+        if (__any_sync(0xFFFFFFFFu, bad)) {
+          // A NaN value that some rows may not see: which (16-dim block, row)
+          // pairs see one, as an MMA of 0/1 operands; then it leaves the product.
+          constexpr uint32_t kOne = 0x3C00u;
+          uint32_t a[4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t two = 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              if ((sb[2 * h + c] & 0x7Fu) == 0x7Fu) {
+                two |= kOne << (16 * c);
+                sb[2 * h + c] = 0;
+              }
+            a[2 * h] = a[2 * h + 1] = two;
+          }
+          const int kt = k0 + 16 * u + t;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const int see = keys_of_row(8 * n + g);
+            uint32_t b[2];
+            float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              b[h] = (kt + 8 * h < see ? kOne : 0u) | (kt + 8 * h + 4 < see ? kOne << 16 : 0u);
+            mma16816(hit, a, b[0], b[1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              if (hit[c] > 0.0f) {
+#pragma unroll
+                for (int i = 0; i < kDM; ++i) o[n][i][c] = o[n][i][2 + c] = __uint_as_float(0x7FC00000u);
+              }
           }
         }
       }
-    }
+      const __half2 s01 = e4m3x2_to_half2(sb[0] | (sb[1] << 8)), s23 = e4m3x2_to_half2(sb[2] | (sb[3] << 8));
+      uint32_t vw[4][D / 64];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const float base = mx[m][hf] == -INFINITY ? 0.0f : mx[m][hf];
-        float e[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          e[c] = ex2(s[m][c >> 1][2 * hf + (c & 1)] - base);
-          sum[m][hf] += e[c];
-        }
-        pa[m][hf] = half2u(e[0], e[1]);
-        pa[m][2 + hf] = half2u(e[2], e[3]);
-      }
-    }
-
-    // ---- values: lane (g, t) takes dims kDG g .. of keys t, 4+t, 8+t, 12+t
-    const uint8_t* vs = st + 2 * kCode + kScale + (D == 128 ? g : g >> 1);
-    uint32_t sb[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) sb[c] = vs[(t + 4 * c) * (D / 16)];
-    if (masked) {
-      bool bad = false;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) bad |= (sb[c] & 0x7Fu) == 0x7Fu;
-      if (__any_sync(0xFFFFFFFFu, bad)) {
-        // A NaN value that some rows may not see: which (row, 16-dim block)
-        // pairs see one, as an MMA of 0/1 operands; then it leaves the product.
-        constexpr uint32_t kOne = 0x3C00u;
-        uint32_t b[2];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          b[nt] = 0;
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            if ((sb[2 * nt + c] & 0x7Fu) == 0x7Fu) {
-              b[nt] |= kOne << (16 * c);
-              sb[2 * nt + c] = 0;
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          uint32_t a[4];
-          float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-              a[2 * nt + hf] = (k0 + 8 * nt + t < lim[m][hf] ? kOne : 0u) |
-                               (k0 + 8 * nt + 4 + t < lim[m][hf] ? kOne << 16 : 0u);
-          mma16816(hit, a, b[0], b[1]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (hit[c] > 0.0f) {
-#pragma unroll
-              for (int i = 0; i < kDG; ++i) o[m][i][c] = __uint_as_float(0x7FC00000u);
-            }
+      for (int c = 0; c < 4; ++c) {
+        const uint8_t* src = st + kCode + (16 * u + t + 4 * c) * (D / 2) + g * (D / 16);
+        if (D == 128) {
+          const uint2 w = *reinterpret_cast<const uint2*>(src);
+          vw[c][0] = w.x, vw[c][D / 64 - 1] = w.y;
+        } else {
+          vw[c][0] = *reinterpret_cast<const uint32_t*>(src);
         }
       }
-    }
-    const __half2 s01 = e4m3x2_to_half2(sb[0] | (sb[1] << 8)), s23 = e4m3x2_to_half2(sb[2] | (sb[3] << 8));
-    uint32_t vw[4][D / 64];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint8_t* src = st + kCode + (t + 4 * c) * (D / 2) + g * (D / 16);
-      if (D == 128) {
-        const uint2 w = *reinterpret_cast<const uint2*>(src);
-        vw[c][0] = w.x, vw[c][D / 64 - 1] = w.y;
-      } else {
-        vw[c][0] = *reinterpret_cast<const uint32_t*>(src);
-      }
-    }
+      for (int h = 0; h < D / 64; ++h) {
+        uint32_t ev[2][4], od[2][4];
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h) {
-      uint32_t ev[2][4], od[2][4];
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t a = vw[2 * q][h], b = vw[2 * q + 1][h];
+          e2m1x8_to_f16x8((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), ev[q]);
+          e2m1x8_to_f16x8(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), od[q]);
+        }
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const uint32_t a = vw[2 * nt][h], b = vw[2 * nt + 1][h];
-        e2m1x8_to_f16x8((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), ev[nt]);
-        e2m1x8_to_f16x8(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), od[nt]);
-      }
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a[4] = {hmul2u(ev[0][j], s01), hmul2u(od[0][j], s01), hmul2u(ev[1][j], s23),
+                                 hmul2u(od[1][j], s23)};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t e0 = hmul2u(ev[0][j], s01), e1 = hmul2u(ev[1][j], s23);
-        const uint32_t d0 = hmul2u(od[0][j], s01), d1 = hmul2u(od[1][j], s23);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma16816(o[m][8 * h + 2 * j], pa[m], e0, e1);
-          mma16816(o[m][8 * h + 2 * j + 1], pa[m], d0, d1);
+          for (int n = 0; n < NT; ++n) mma16816(o[n][4 * h + j], a, pb[u][n][0], pb[u][n][1]);
         }
       }
     }
@@ -411,26 +473,24 @@ __global__ void __launch_bounds__(kThreadsA, MT == 1 ? 3 : 2)
   }
   cp_wait<0>();
 
-  // ---- join the four warps: o holds dims kDG * (2t), kDG * (2t+1) onward of rows g, g + 8
+  // ---- join the four warps: o[n][i] holds dims D/8 g + 2i (c 0, 1) and + 2i + 1 (c 2, 3) of rows 2t, 2t + 1
   float* jo = reinterpret_cast<float*>(smem);
   float2* jm = reinterpret_cast<float2*>(smem + kWarpsA * kRows * (D + 4) * 4);
   __syncthreads();                                        // every warp has left its ring
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float v = sum[m][hf];
-      v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-      v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-      const int r = 16 * m + 8 * hf + g;
-      if (t == 0) jm[warp * kRows + r] = make_float2(mx[m][hf], v);
-      float* dst = jo + (warp * kRows + r) * (D + 4);
+    for (int c = 0; c < 2; ++c) {
+      float v = sum[n][c];
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+      const int r = 8 * n + 2 * t + c;
+      if (g == 0) jm[warp * kRows + r] = make_float2(ref[n][c], v);
+      float* dst = jo + (warp * kRows + r) * (D + 4) + (D / 8) * g;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int i = 0; i < kDG; i += 4)
-          *reinterpret_cast<float4*>(dst + kDG * (2 * t + c) + i) =
-              make_float4(o[m][i][2 * hf + c], o[m][i + 1][2 * hf + c], o[m][i + 2][2 * hf + c], o[m][i + 3][2 * hf + c]);
+      for (int i = 0; i < kDM; i += 2)
+        *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(o[n][i][c], o[n][i][2 + c], o[n][i + 1][c], o[n][i + 1][2 + c]);
     }
   __syncthreads();
   constexpr int kVec = D / 8;
@@ -453,10 +513,10 @@ __global__ void __launch_bounds__(kThreadsA, MT == 1 ? 3 : 2)
     }
     const int row = rt.row0 + r, tok = row / group, head = kvh * group + row - tok * group;
     const long long token = rt.token0 + tok;
-    if (active == 1) {
+    if (whole) {
       store_row8<BF16>(p, token, head, d0, v, top, total);
     } else {
-      const long long at = ((long long)part * p.tokens + token) * p.q_heads + head;
+      const long long at = part * kRows + r;
       float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + d0);
       dst[0] = make_float4(v[0], v[1], v[2], v[3]);
       dst[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -465,99 +525,231 @@ __global__ void __launch_bounds__(kThreadsA, MT == 1 ? 3 : 2)
   }
 }
 
-// Joins the parts of the key axis, in order: D/8 threads per (token, head).
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ Kv4AttnLaunch p, int tile_rows) {
+__device__ __forceinline__ Kv4Work work_of(const Kv4AttnLaunch& p, int tile_rows) {
+  Kv4Work w;
+  w.q_start = p.q_start;
+  w.kv_len = p.kv_len;
+  w.requests = p.requests;
+  w.tokens = p.tokens;
+  w.group = p.q_heads / p.c.heads;
+  w.heads = p.c.heads;
+  w.tile_rows = tile_rows;
+  w.causal = p.causal;
+  w.max_rows = p.max_rows;
+  w.capacity = (long long)p.max_pages << p.c.page_log2;
+  return w;
+}
+
+template <int D, int NT, bool BF16>
+__global__ void __launch_bounds__(kThreadsA, ctas_per_sm(NT))
+    kv4_attention_kernel(const __grid_constant__ Kv4AttnLaunch p) {
   griddep_wait();
-  constexpr int kVec = D / 8, kPer = 128 / kVec;
-  const int group = p.q_heads / p.c.heads;
-  const long long i = (long long)blockIdx.x * kPer + threadIdx.x / kVec;
-  if (i >= (long long)p.tokens * p.q_heads) return;
-  const int token = (int)(i / p.q_heads), head = (int)(i % p.q_heads), d0 = 8 * (threadIdx.x % kVec);
-  const int last_key = find_last_key(p.q_start, p.kv_len, p.requests, p.tokens, token, group, head % group, tile_rows,
-                                     (long long)p.max_pages << p.c.page_log2, p.causal);
-  if (last_key < 0) return;                               // behind the last sequence
-  const int active = active_parts(last_key, p.splits, p.chunk);
-  if (active == 1) return;                                // written by the first kernel
-  const long long step = (long long)p.tokens * p.q_heads;
-  float top = -INFINITY, total = 0.0f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int s = 0; s < active; ++s) top = fmaxf(top, p.part_ml[s * step + i].x);
-  for (int s = 0; s < active; ++s) {
-    const float2 ml = p.part_ml[s * step + i];
-    const float f = ex2_diff(ml.x, top);
-    total = fmaf(ml.y, f, total);
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + (s * step + i) * D + d0);
-    const float4 a = src[0], b = src[1];
-    v[0] = fmaf(a.x, f, v[0]), v[1] = fmaf(a.y, f, v[1]), v[2] = fmaf(a.z, f, v[2]), v[3] = fmaf(a.w, f, v[3]);
-    v[4] = fmaf(b.x, f, v[4]), v[5] = fmaf(b.y, f, v[5]), v[6] = fmaf(b.z, f, v[6]), v[7] = fmaf(b.w, f, v[7]);
+  griddep_launch_dependents();
+  const Kv4Work w = work_of(p, 8 * NT);
+  const WarpUnits wu = warp_units(w);
+  const long long per = (wu.total + gridDim.x - 1) / gridDim.x;
+  const long long u0 = per * blockIdx.x, u1 = min(u0 + per, wu.total);
+  for (long long u = u0; u < u1;) {
+    long long first;
+    const int b = request_of_unit(w, wu, u, &first);
+    const Segment sg = segment_in(w, span_of(w, b), b, u - first);
+    const int n = (int)min((long long)(sg.units - sg.unit0), u1 - u);
+    const bool whole = n == sg.units;
+    attend_segment<D, NT, BF16>(p, sg.tile, sg.head, sg.unit0 * kUnitKeys,
+                                min(sg.tile.last_key, (sg.unit0 + n) * kUnitKeys), whole,
+                                2ll * blockIdx.x + (u == u0 ? 0 : 1));
+    u += n;
+    __syncthreads();                                      // shared memory changes hands
   }
-  store_row8<BF16>(p, token, head, d0, v, top, total);
+}
+
+// Joins the parts of segments that several CTAs took: WR warps (1 or all 8 of
+// the CTA) for one (token, head) at a time.  Warp w of them adds parts w, w +
+// WR, ..., eight in flight, and the warps' sums are added in order.  Where the
+// parts lie follows from the lengths alone, and is worked out while the first
+// kernel still runs (it lets this one start only after what precedes both has
+// ended).
+constexpr int kWarpsJ = 8;
+template <int D, int NT, int WR, bool BF16>
+__global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_kernel(const __grid_constant__ Kv4AttnLaunch p) {
+  constexpr int kVec = D / 32, kFlight = 8;               // floats a lane, parts in flight
+  __shared__ float acc[kWarpsJ][D];
+  __shared__ float2 sums[kWarpsJ];
+  const Kv4Work w = work_of(p, 8 * NT);
+  const WarpUnits wu = warp_units(w);
+  const long long per = (wu.total + p.ctas - 1) / p.ctas;
+  const int lane = threadIdx.x & 31, team = (threadIdx.x >> 5) / WR, warp = (threadIdx.x >> 5) % WR;
+  const long long rows = (long long)p.tokens * p.q_heads;
+  bool waited = false;
+  // (With WR = 8 all of the CTA's warps take the same rows and the same branches.)
+  for (long long i = (long long)blockIdx.x * (kWarpsJ / WR) + team; i < rows; i += (long long)gridDim.x * (kWarpsJ / WR)) {
+    const int token = (int)(i / p.q_heads), head = (int)(i - (long long)token * p.q_heads);
+    const int b = request_of(p.q_start, p.requests, p.tokens, token);
+    if (b < 0) continue;                                  // a token of no request
+    const RequestSpan s = span_of(w, b);
+    const int tok = token - s.token0;
+    if (tok < 0 || tok >= s.n) continue;                  // the request is left out here
+    const int kvh = head / w.group;
+    const long long row = (long long)tok * w.group + head % w.group;
+    int units;
+    const long long first = first_unit_of(w, wu, b) + segment_start(w, s, row, kvh, &units);
+    const int c0 = (int)(first / per), c1 = (int)((first + units - 1) / per);
+    if (c0 == c1) continue;                               // finished by its one CTA
+    const int r = (int)(row % w.tile_rows);
+    const bool late = first != c0 * per;
+    auto part_row = [&](int c) { return (2ll * c + (c == c0 && late ? 1 : 0)) * w.tile_rows + r; };
+    if (!waited) griddep_wait();
+    waited = true;
+    float top = -INFINITY, total = 0.0f, v[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v[j] = 0.0f;
+    for (int c = c0 + warp; c <= c1; c += WR * kFlight) {
+      float2 ml[kFlight];
+      float a[kFlight][kVec];
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q) {
+        const bool there = c + WR * q <= c1;
+        const long long at = part_row(there ? c + WR * q : c);
+        const float* src = p.part_o + at * D + kVec * lane;
+        ml[q] = there ? p.part_ml[at] : make_float2(-INFINITY, 0.0f);
+        if (kVec == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          a[q][0] = x.x, a[q][1] = x.y, a[q][kVec - 2] = x.z, a[q][kVec - 1] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          a[q][0] = x.x, a[q][1] = x.y;
+        }
+      }
+      float to = top;
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q) to = fmaxf(to, ml[q].x);
+      const float f0 = ex2_diff(top, to);
+      top = to;
+      total *= f0;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[j] *= f0;
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q) {
+        if (c + WR * q <= c1) {
+          const float f = ex2_diff(ml[q].x, top);
+          total = fmaf(ml[q].y, f, total);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) v[j] = fmaf(a[q][j], f, v[j]);
+        }
+      }
+    }
+    const int wj = threadIdx.x >> 5;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) acc[wj][kVec * lane + j] = v[j];
+    if (WR == 1) {
+      __syncwarp();
+      if (lane < D / 8) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = acc[wj][8 * lane + j];
+        store_row8<BF16>(p, token, head, 8 * lane, y, top, total);
+      }
+      __syncwarp();
+      continue;
+    }
+    if (lane == 0) sums[wj] = make_float2(top, total);
+    __syncthreads();
+    if (threadIdx.x < D / 8) {
+      float y[8];
+      top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kWarpsJ; ++k) top = fmaxf(top, sums[k].x);
+      total = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kWarpsJ; ++k) {
+        const float f = ex2_diff(sums[k].x, top);
+        total = fmaf(sums[k].y, f, total);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = fmaf(acc[k][8 * threadIdx.x + j], f, y[j]);
+      }
+      store_row8<BF16>(p, token, head, 8 * threadIdx.x, y, top, total);
+    }
+    __syncthreads();
+  }
+  // Every CTA waits, so that this kernel's end implies the first one's.
+  if (!waited) griddep_wait();
+  griddep_launch_dependents();
 }
 
 int tile_rows_for(const Kv4AttnLaunch& p) {
   const int group = p.q_heads / p.c.heads;
-  // Rows of an average request; 32-row tiles dequantize each key once for twice the rows.
-  return (long long)p.tokens * group > 16ll * p.requests ? 32 : 16;
-}
-long long row_tiles_for(const Kv4AttnLaunch& p, int rows) {
-  return max_row_tiles(p.tokens, p.requests, p.q_heads / p.c.heads, rows, p.q_start != nullptr);
+  // The smallest tile that holds an average request's rows: a larger one
+  // dequantizes each key for more rows at once, a smaller one leaves room for
+  // more warps.
+  const long long rows = (long long)p.tokens * group;
+  return rows <= 8ll * p.requests ? 8 : rows <= 16ll * p.requests ? 16 : 32;
 }
 
-template <int D, int MT, bool BF16>
-cudaError_t launch_mt(const Kv4AttnLaunch& p, cudaStream_t stream) {
-  constexpr int kSmem = smem_bytes<D, MT>();
-  cudaError_t e = ensure_smem_limit(kv4_attention_kernel<D, MT, BF16>, kSmem);
-  if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)row_tiles_for(p, 16 * MT), (unsigned)p.splits, (unsigned)p.c.heads);
-  kv4_attention_kernel<D, MT, BF16><<<grid, kThreadsA, kSmem, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || p.splits == 1) return e;
+template <typename... Args>
+cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                         const Kv4AttnLaunch& p) {
   cudaLaunchConfig_t cfg = {};
-  constexpr int kPer = 128 / (D / 8);
-  cfg.gridDim = dim3((unsigned)(((long long)p.tokens * p.q_heads + kPer - 1) / kPer));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, BF16>, p, 16 * MT);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int D, int NT, bool BF16>
+cudaError_t launch_nt(const Kv4AttnLaunch& p, cudaStream_t stream) {
+  constexpr int kSmem = smem_bytes<D, NT>();
+  cudaError_t e = ensure_smem_limit(kv4_attention_kernel<D, NT, BF16>, kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_after(kv4_attention_kernel<D, NT, BF16>, dim3((unsigned)p.ctas), kThreadsA, kSmem, stream, p);
+  if (e != cudaSuccess || !p.join) return e;
+  const long long rows = (long long)p.tokens * p.q_heads;
+  // A warp a row while a row has a few parts, eight for the many parts of few long sequences.
+  const bool many = p.ctas > 8 * p.segments;
+  const long long teams = many ? rows : (rows + kWarpsJ - 1) / kWarpsJ, most = 8ll * p.num_sms;
+  const dim3 grid((unsigned)(teams < most ? teams : most));
+  return many ? launch_after(kv4_join_kernel<D, NT, kWarpsJ, BF16>, grid, 32 * kWarpsJ, 0, stream, p)
+              : launch_after(kv4_join_kernel<D, NT, 1, BF16>, grid, 32 * kWarpsJ, 0, stream, p);
 }
 
 template <int D, bool BF16>
 cudaError_t launch_d(const Kv4AttnLaunch& p, cudaStream_t stream) {
-  return tile_rows_for(p) == 16 ? launch_mt<D, 1, BF16>(p, stream) : launch_mt<D, 2, BF16>(p, stream);
+  if (p.tile_rows == 8) return launch_nt<D, 1, BF16>(p, stream);
+  if (p.tile_rows == 16) return launch_nt<D, 2, BF16>(p, stream);
+  return launch_nt<D, 4, BF16>(p, stream);
 }
 
 }  // namespace
 
-void kv4_attention_plan(Kv4AttnLaunch& p, int max_kv) {
-  // Parts of the key axis: enough CTAs for about three an SM, at least one
-  // 16-key tile a warp each.
-  const int rows = tile_rows_for(p);
-  const long long ctas = row_tiles_for(p, rows) * p.c.heads, want = 3 * 148;
-  const int step = kTileA * kWarpsA;
-  if (max_kv < 1) max_kv = 1;
-  long long parts = (want + ctas - 1) / ctas;
-  const long long most = (max_kv + step - 1) / step;
-  if (parts > most) parts = most;
-  if (parts > 128) parts = 128;
-  if (parts < 1) parts = 1;
-  p.chunk = (int)(((max_kv + parts - 1) / parts + step - 1) / step * step);
-  p.splits = (max_kv + p.chunk - 1) / p.chunk;
+void kv4_attention_plan(Kv4AttnLaunch& p, int max_kv, int num_sms) {
+  p.num_sms = num_sms;
+  p.tile_rows = tile_rows_for(p);
+  p.max_rows = 0x7FFFFFFF;
+  // One resident set of CTAs shares the
+  // work evenly, whatever the lengths; no more CTAs than units of work.
+  p.segments = max_units(p.tokens, p.requests, p.q_heads / p.c.heads, p.c.heads, p.tile_rows, p.q_start != nullptr, 0);
+  const long long units = p.segments * tile_units(max_kv);
+  const long long slots = (long long)num_sms * ctas_per_sm(p.tile_rows / 8);
+  p.ctas = (int)(units < slots ? (units > 0 ? units : 1) : slots);
+  // One CTA, or tables that hold one unit at most: no segment is ever cut.
+  p.join = p.ctas > 1 && ((long long)p.max_pages << p.c.page_log2) > kUnitKeys;
 }
 
 size_t kv4_attention_workspace(const Kv4AttnLaunch& p) {
-  if (p.splits <= 1) return 0;
-  return (size_t)p.splits * p.tokens * p.q_heads * ((size_t)p.c.D * 4 + 8);
+  return p.join ? (size_t)p.ctas * 2 * p.tile_rows * ((size_t)p.c.D * 4 + 8) : 0;
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnLaunch& p0, void* workspace, cudaStream_t stream) {
   Kv4AttnLaunch p = p0;
   p.part_o = static_cast<float*>(workspace);
-  p.part_ml = p.splits > 1 ? reinterpret_cast<float2*>(p.part_o + (size_t)p.splits * p.tokens * p.q_heads * p.c.D)
-                           : nullptr;
+  p.part_ml = p.join ? reinterpret_cast<float2*>(p.part_o + (size_t)p.ctas * 2 * p.tile_rows * p.c.D) : nullptr;
   if (p.c.D == 128)
     return p.dtype == 0 ? launch_d<128, true>(p, stream) : launch_d<128, false>(p, stream);
   return p.dtype == 0 ? launch_d<64, true>(p, stream) : launch_d<64, false>(p, stream);

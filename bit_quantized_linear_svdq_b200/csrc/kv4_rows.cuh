@@ -35,7 +35,7 @@ KV4_HD RequestSpan request_span(const int* q_start, const int* kv_len, int reque
     s.n = tokens / requests;
     s.token0 = b * s.n;
   }
-  s.keys = kv4_min(kv4_max(kv_len[b], 0), capacity);
+  s.keys = kv_len ? kv4_min(kv4_max(kv_len[b], 0), capacity) : 0;
   return s;
 }
 
@@ -44,26 +44,13 @@ KV4_HD int keys_seen(int keys, int n, int i, int causal) {
   return causal ? kv4_max((long long)keys - n + i + 1, 0) : keys;
 }
 
-// Number of row tiles to launch: exact without q_start, an upper bound with it
-// (sum of ceil(n_b group / rows) with sum of n_b = tokens).
-KV4_HD long long max_row_tiles(int tokens, int requests, int group, int rows, bool ragged) {
-  if (!ragged) return requests * (((long long)(tokens / requests) * group + rows - 1) / rows);
-  return ((long long)tokens * group + (long long)requests * (rows - 1)) / rows;
-}
-
-// Parts of the key axis that a tile with `last_key` keys uses.
-KV4_HD int active_parts(int last_key, int splits, int chunk) {
-  const int need = last_key > 0 ? (last_key - 1) / chunk + 1 : 1;
-  return need < splits ? need : splits;
-}
-
+// A tile: `tile_rows` consecutive rows of a request under one key head.
 struct RowTile {
   int request, token0, n, keys;                 // of the request
   int row0, rows;                               // of the tile; rows == 0: nothing to do
   int last_key;                                 // keys that its last row sees
   KV4_HD int keys_of(int tok, int causal) const { return keys_seen(keys, n, tok, causal); }
 };
-
 KV4_HD RowTile tile_of(const RequestSpan& s, int b, int group, int tile_rows, long long tile, int causal) {
   RowTile r;
   r.request = b;
@@ -77,23 +64,65 @@ KV4_HD RowTile tile_of(const RequestSpan& s, int b, int group, int tile_rows, lo
   return r;
 }
 
-// Row tile number `tile` of the launch, one thread at a time (host form).
-KV4_HD RowTile find_row_tile_serial(const int* q_start, const int* kv_len, int requests, int tokens, int group,
-                                    int tile_rows, long long tile, long long capacity, int causal) {
-  for (int b = 0; b < requests; ++b) {
-    const RequestSpan s = request_span(q_start, kv_len, requests, tokens, b, capacity);
-    const long long nt = ((long long)s.n * group + tile_rows - 1) / tile_rows;
-    if (tile < nt) return tile_of(s, b, group, tile_rows, tile, causal);
-    tile -= nt;
-  }
-  RowTile r = {};
-  return r;
+// The work of one launch, cut into equal shares.  A segment is a tile under
+// one key head, a unit 128 of its keys (at least one unit, so that rows without
+// keys are written too).  Units are numbered by request, head, tile, key; CTA
+// c takes units c * per .. (c + 1) * per.  A segment that lies in one share is
+// finished there; otherwise each of its CTAs leaves a part, in slot 0 if the
+// segment covers the share's first unit and in slot 1 if it starts later (at
+// most one of each a CTA).
+constexpr int kUnitKeys = 128;
+struct Kv4Work {
+  const int *q_start, *kv_len;
+  int requests, tokens, group, heads, tile_rows, causal;
+  int max_rows;                                 // requests with more rows are left out
+  long long capacity;                           // keys that a block table can hold
+};
+KV4_HD RequestSpan span_of(const Kv4Work& w, int b) {
+  RequestSpan s = request_span(w.q_start, w.kv_len, w.requests, w.tokens, b, w.capacity);
+  if ((long long)s.n * w.group > w.max_rows) s.n = 0;
+  return s;
 }
-
-// Keys that the last row of the tile sees that holds head `in_group` of query
-// token `token`; -1: no request has the token.
-KV4_HD int find_last_key(const int* q_start, const int* kv_len, int requests, int tokens, int token, int group,
-                         int in_group, int tile_rows, long long capacity, int causal) {
+KV4_HD int tile_units(int last_key) { return last_key > 0 ? (last_key - 1) / kUnitKeys + 1 : 1; }
+KV4_HD int tiles_of(const Kv4Work& w, const RequestSpan& s) {
+  return (int)(((long long)s.n * w.group + w.tile_rows - 1) / w.tile_rows);
+}
+// Units of a request under one head.
+KV4_HD long long head_units(const Kv4Work& w, const RequestSpan& s) {
+  const int nt = tiles_of(w, s);
+  long long u = 0;
+  for (int t = 0; t < nt; ++t) u += tile_units(tile_of(s, 0, w.group, w.tile_rows, t, w.causal).last_key);
+  return u;
+}
+struct Segment {
+  RowTile tile;
+  int head, units, unit0;                       // units of the segment; the wanted unit's place in it
+};
+// Unit `u` of request b (u < heads * head_units).
+KV4_HD Segment segment_in(const Kv4Work& w, const RequestSpan& s, int b, long long u) {
+  const long long per_head = head_units(w, s);
+  Segment g;
+  g.head = (int)(u / per_head);
+  u -= g.head * per_head;
+  for (int t = 0;; ++t) {
+    g.tile = tile_of(s, b, w.group, w.tile_rows, t, w.causal);
+    g.units = tile_units(g.tile.last_key);
+    if (u < g.units) break;
+    u -= g.units;
+  }
+  g.unit0 = (int)u;
+  return g;
+}
+// First unit of the segment that holds row `row` of request b under `head`, from the request's first unit.
+KV4_HD long long segment_start(const Kv4Work& w, const RequestSpan& s, long long row, int head, int* units) {
+  const int tile = (int)(row / w.tile_rows);
+  long long u = head * head_units(w, s);
+  for (int t = 0; t < tile; ++t) u += tile_units(tile_of(s, 0, w.group, w.tile_rows, t, w.causal).last_key);
+  *units = tile_units(tile_of(s, 0, w.group, w.tile_rows, tile, w.causal).last_key);
+  return u;
+}
+// The request that holds query token `token`, or -1.
+KV4_HD int request_of(const int* q_start, int requests, int tokens, int token) {
   int b;
   if (q_start) {
     // The last request that starts at or before the token (starts ascend).
@@ -104,58 +133,78 @@ KV4_HD int find_last_key(const int* q_start, const int* kv_len, int requests, in
       else hi = mid;
     }
     b = lo - 1;
-    if (b < 0) return -1;
   } else {
     const int n = tokens / requests;
-    b = n > 0 ? token / n : requests;
-    if (b >= requests) return -1;
+    b = n > 0 ? token / n : -1;
   }
-  const RequestSpan s = request_span(q_start, kv_len, requests, tokens, b, capacity);
-  if (token < s.token0 || token >= s.token0 + s.n) return -1;
-  const long long row = (long long)(token - s.token0) * group + in_group;
-  return tile_of(s, b, group, tile_rows, row / tile_rows, causal).last_key;
+  if (b < 0 || b >= requests) return -1;
+  const RequestSpan s = request_span(q_start, nullptr, requests, tokens, b, 0);
+  return token >= s.token0 && token < s.token0 + s.n ? b : -1;
+}
+// Upper bound of the units of a launch whose requests have at most `max_kv` keys.
+KV4_HD long long max_units(int tokens, int requests, int group, int heads, int tile_rows, bool ragged, int max_kv) {
+  const long long tiles = ragged ? ((long long)tokens * group + (long long)requests * (tile_rows - 1)) / tile_rows
+                                 : requests * (((long long)(tokens / requests) * group + tile_rows - 1) / tile_rows);
+  return tiles * heads * tile_units(max_kv);
 }
 
 #if defined(__CUDACC__)
-// The same as find_row_tile_serial, by a warp: 32 requests at a time.  Every
-// lane of the warp calls it with the same arguments and gets the same answer.
-__device__ __forceinline__ RowTile find_row_tile(const int* q_start, const int* kv_len, int requests, int tokens,
-                                                 int group, int tile_rows, long long tile, long long capacity,
-                                                 int causal) {
-  if (!q_start) {
-    const long long per = ((long long)(tokens / requests) * group + tile_rows - 1) / tile_rows;
-    const int b = per > 0 ? (int)(tile / per) : requests;
-    RowTile r = {};
-    if (b >= requests) return r;
-    return tile_of(request_span(nullptr, kv_len, requests, tokens, b, capacity), b, group, tile_rows, tile % per,
-                   causal);
+// Warp-wide view of the launch's units: total, and the first unit of a request.
+// Every lane calls with the same arguments.
+struct WarpUnits {
+  long long total;
+  long long mine, upto;                         // requests <= 32: units of request `lane`, inclusive prefix
+};
+__device__ __forceinline__ long long warp_prefix(long long v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += x;
   }
+  return v;
+}
+__device__ __forceinline__ long long units_of_request(const Kv4Work& w, int b) {
+  return b < w.requests ? head_units(w, span_of(w, b)) * w.heads : 0;
+}
+__device__ __forceinline__ WarpUnits warp_units(const Kv4Work& w) {
+  const int lane = threadIdx.x & 31;
+  WarpUnits r;
+  r.total = 0;
+  for (int b0 = 0; b0 < w.requests; b0 += 32) {
+    r.mine = units_of_request(w, b0 + lane);
+    r.upto = warp_prefix(r.mine);
+    r.total += __shfl_sync(0xFFFFFFFFu, r.upto, 31);
+  }
+  return r;
+}
+// Request that holds unit u (< total), and that request's first unit.
+__device__ __forceinline__ int request_of_unit(const Kv4Work& w, const WarpUnits& r, long long u, long long* first) {
   const int lane = threadIdx.x & 31;
   long long before = 0;
-  for (int b0 = 0; b0 < requests; b0 += 32) {
-    const int b = b0 + lane;
-    long long nt = 0;
-    if (b < requests) {
-      const RequestSpan s = request_span(q_start, kv_len, requests, tokens, b, capacity);
-      nt = ((long long)s.n * group + tile_rows - 1) / tile_rows;
-    }
-    long long upto = nt;                        // inclusive prefix sum
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const unsigned hit = __ballot_sync(0xFFFFFFFFu, tile < before + upto);
+  for (int b0 = 0; b0 < w.requests; b0 += 32) {
+    const long long mine = w.requests <= 32 ? r.mine : units_of_request(w, b0 + lane);
+    const long long upto = w.requests <= 32 ? r.upto : warp_prefix(mine);
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, u < before + upto);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      const long long first = before + __shfl_sync(0xFFFFFFFFu, upto - nt, l);
-      return tile_of(request_span(q_start, kv_len, requests, tokens, b0 + l, capacity), b0 + l, group, tile_rows,
-                     tile - first, causal);
+      *first = before + __shfl_sync(0xFFFFFFFFu, upto - mine, l);
+      return b0 + l;
     }
     before += __shfl_sync(0xFFFFFFFFu, upto, 31);
   }
-  RowTile r = {};
-  return r;
+  *first = before;
+  return w.requests - 1;
+}
+// First unit of request b.
+__device__ __forceinline__ long long first_unit_of(const Kv4Work& w, const WarpUnits& r, int b) {
+  const int lane = threadIdx.x & 31;
+  long long before = 0;
+  for (int b0 = 0; b0 + 31 < b; b0 += 32) before += __shfl_sync(0xFFFFFFFFu, warp_prefix(units_of_request(w, b0 + lane)), 31);
+  const int b0 = b & ~31;
+  const long long mine = w.requests <= 32 ? r.mine : units_of_request(w, b0 + lane);
+  const long long upto = w.requests <= 32 ? r.upto : warp_prefix(mine);
+  return before + __shfl_sync(0xFFFFFFFFu, upto - mine, b & 31);
 }
 #endif
 
