@@ -30,6 +30,7 @@ __all__ = [
     "qk_norm_rope", "rope_frequencies", "KV4Cache", "kv4_cache", "kv4_append", "kv4_read", "kv4_attention",
     "svdq_heads", "svdq_qk_norm_rope_desc", "svdq_kv4_cache", "svdq_kv4_attention_desc", "svdq_qk_norm_rope",
     "svdq_kv4_append", "svdq_kv4_read", "svdq_kv4_attention_workspace_bytes", "svdq_kv4_attention",
+    "svdq_kv4_attention_status",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -120,6 +121,7 @@ def load_library() -> ctypes.CDLL:
         "svdq_kv4_read": (ci, [vp, vp, vp, ci, ci, vp, vp]),
         "svdq_kv4_attention_workspace_bytes": (cs, [vp]),
         "svdq_kv4_attention": (ci, [vp, vp, cs, vp]),
+        "svdq_kv4_attention_status": (ci, [ctypes.POINTER(ci)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -472,5 +474,6 @@ class SVDQLinear:
 
 from .attention import (KV4Cache, kv4_append, kv4_attention, kv4_cache, kv4_read, qk_norm_rope,  # noqa: E402
                         rope_frequencies, svdq_heads, svdq_kv4_append, svdq_kv4_attention,
-                        svdq_kv4_attention_desc, svdq_kv4_attention_workspace_bytes, svdq_kv4_cache,
+                        svdq_kv4_attention_desc, svdq_kv4_attention_status,
+                        svdq_kv4_attention_workspace_bytes, svdq_kv4_cache,
                         svdq_kv4_read, svdq_qk_norm_rope, svdq_qk_norm_rope_desc)

@@ -89,6 +89,14 @@ def svdq_kv4_attention(desc: svdq_kv4_attention_desc, workspace_ptr, workspace_b
                                                          _base._stream(stream)), "svdq_kv4_attention")
 
 
+def svdq_kv4_attention_status() -> int:
+    flags = ctypes.c_int(0)
+    st = _base.load_library().svdq_kv4_attention_status(ctypes.byref(flags))
+    if st not in (0, 6):
+        raise _base.SvdqError(st, "svdq_kv4_attention_status")
+    return flags.value
+
+
 # ----------------------------------------------------------------- argument checks
 
 def _device_of(**tensors) -> torch.device:

@@ -93,7 +93,9 @@ svdq_status check_rows(const svdq_kv4_cache* cache, const svdq_heads* k, const s
   return SVDQ_OK;
 }
 
-svdq_status check_attention(const svdq_kv4_attention_desc* d, svdq::Kv4AttnLaunch* p) {
+svdq_status check_attention(const svdq_kv4_attention_desc* d, svdq::Kv4Plan* plan) {
+  svdq::Kv4AttnLaunch launch = {}, *p = &launch;
+  plan->use_few = plan->use_many = false;
   if (!d) return fail(SVDQ_ERR_INVALID_ARG, "null description");
   svdq_status s = check_cache(&d->cache, &p->c);
   if (s != SVDQ_OK) return s;
@@ -125,18 +127,10 @@ svdq_status check_attention(const svdq_kv4_attention_desc* d, svdq::Kv4AttnLaunc
   p->dtype = d->dtype;
   p->causal = d->causal != 0;
   p->scale = d->softmax_scale;
-  p->num_sms = 0;
-  p->tile_rows = 8;
-  p->max_rows = 0;
-  p->segments = 0;
-  p->ctas = 1;
-  p->join = 0;
-  p->part_o = nullptr;
-  p->part_ml = nullptr;
   if (d->tokens > 0 && d->requests > 0) {
     const long long cap = (long long)d->max_pages << p->c.page_log2;
     const long long bound = d->max_kv_len > 0 && d->max_kv_len < cap ? d->max_kv_len : cap;
-    svdq::kv4_attention_plan(*p, (int)bound, num_sms());
+    *plan = svdq::kv4_attention_plan(launch, (int)bound, num_sms());
   }
   return SVDQ_OK;
 }
@@ -206,14 +200,14 @@ svdq_status svdq_kv4_read(const svdq_kv4_cache* cache, const svdq_heads* k_out, 
 }
 
 size_t svdq_kv4_attention_workspace_bytes(const svdq_kv4_attention_desc* d) {
-  svdq::Kv4AttnLaunch p;
+  svdq::Kv4Plan p;
   if (check_attention(d, &p) != SVDQ_OK) return 0;
   return svdq::kv4_attention_workspace(p);
 }
 
 svdq_status svdq_kv4_attention(const svdq_kv4_attention_desc* d, void* workspace, size_t workspace_bytes,
                                void* stream) {
-  svdq::Kv4AttnLaunch p;
+  svdq::Kv4Plan p;
   svdq_status s = check_attention(d, &p);
   if (s != SVDQ_OK || d->tokens == 0 || d->requests == 0) return s;
   if ((s = check_heads(d->q)) != SVDQ_OK || (s = check_heads(d->out)) != SVDQ_OK) return s;
@@ -225,6 +219,14 @@ svdq_status svdq_kv4_attention(const svdq_kv4_attention_desc* d, void* workspace
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return fail(SVDQ_ERR_WORKSPACE, "workspace null, too small or not 16-byte aligned");
   return launched(svdq::launch_kv4_attention(p, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+svdq_status svdq_kv4_attention_status(int* flags) {
+  if (!flags) return SVDQ_ERR_INVALID_ARG;
+  unsigned word = 0;
+  const svdq_status s = launched(svdq::kv4_attention_status(&word));
+  *flags = (int)word;
+  return s != SVDQ_OK ? s : word ? SVDQ_ERR_DEVICE : SVDQ_OK;
 }
 
 }  // extern "C"

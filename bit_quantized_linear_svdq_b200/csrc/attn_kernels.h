@@ -49,6 +49,12 @@ struct Kv4RowsLaunch {
 cudaError_t launch_kv4_append(const Kv4RowsLaunch& p, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4RowsLaunch& p, cudaStream_t stream);
 
+// A segment that a CTA began and another one goes on with (rows 0: none).
+struct Kv4Cut {
+  int token0, row0, rows;         // of the request; of the tile
+  int head, last_cta, slot;       // key head; CTA that ends it; the beginner's part
+  int pad[2];
+};
 struct Kv4AttnLaunch {
   Kv4Cache c;
   const void* q;
@@ -63,16 +69,26 @@ struct Kv4AttnLaunch {
   float scale;                    // softmax scale
   // Set by kv4_attention_plan:
   int num_sms;
-  int tile_rows, max_rows;        // rows of a tile (8, 16, 32); requests with more rows are left out
+  int tile_rows;                  // rows of a tile: 8, 16, 32 or 256
+  int min_rows, max_rows;         // requests with fewer or more rows are left out
   long long segments;             // tiles x heads, at most
   int ctas, join;                 // CTAs that share the work; whether segments may be cut
   float* part_o;                  // join: (ctas, 2, tile_rows, D) fp32
   float2* part_ml;                //       (ctas, 2, tile_rows) {max, sum} in base 2
+  Kv4Cut* cuts;                   //       (ctas)
+};
+// The launches of one call: requests of few rows and of many (kv4_attention_tc.cu).
+struct Kv4Plan {
+  Kv4AttnLaunch few, many;
+  bool use_few, use_many;
 };
 // `max_kv`: keys a request has at most (for the number of CTAs only).  The
 // launch needs kv4_attention_workspace bytes, 16-byte aligned.
-void kv4_attention_plan(Kv4AttnLaunch& p, int max_kv, int num_sms);
-size_t kv4_attention_workspace(const Kv4AttnLaunch& p);
-cudaError_t launch_kv4_attention(const Kv4AttnLaunch& p, void* workspace, cudaStream_t stream);
+Kv4Plan kv4_attention_plan(const Kv4AttnLaunch& base, int max_kv, int num_sms);
+size_t kv4_attention_workspace(const Kv4Plan& plan);
+cudaError_t launch_kv4_attention(const Kv4Plan& plan, void* workspace, cudaStream_t stream);
+cudaError_t launch_kv4_attention_tc(const Kv4AttnLaunch& p, cudaStream_t stream);
+// Reads and clears the error word of launch_kv4_attention_tc on the current device (synchronizes it).
+cudaError_t kv4_attention_status(unsigned* flags);
 
 }  // namespace svdq

@@ -44,20 +44,14 @@
 // taken out of the product and given to the rows that see it.
 #include <cuda_runtime.h>
 
-#include "attn_kernels.h"
-#include "kv4_codes.cuh"
-#include "kv4_rows.cuh"
-#include "kcommon.cuh"
-#include "ptx.cuh"
+#include "kv4_common.cuh"
 
 namespace svdq {
 namespace {
 
 constexpr int kWarpsA = 4, kThreadsA = 32 * kWarpsA, kTileA = 32, kStagesA = 2;
-constexpr uint32_t kAbsent = 0xFFFFFFFFu;             // no such row: past the keys, or in no page of the cache
 // Resident CTAs an SM by rows of a tile / 8: what the accumulators leave room for.
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
-constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -78,38 +72,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ uint32_t hmul2u(uint32_t a, __half2 b) {
-  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t half2u(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// a x b where a == 0 wins over any b: a factor exp2(-inf - m) of a part that saw nothing.
-__device__ __forceinline__ float ex2_diff(float m, float to) { return m == -INFINITY ? 0.0f : ex2(m - to); }
-
-// One 8-element piece of an output row: v / total in the storage type, and the
-// row's log sum.  total == 0: the row saw no key (or only scores of -inf).
-template <bool BF16>
-__device__ __forceinline__ void store_row8(const Kv4AttnLaunch& p, long long token, int head, int d0,
-                                           const float (&v)[8], float top, float total) {
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w[j] = BF16 ? pack_bf16x2(v[2 * j] * inv, v[2 * j + 1] * inv) : half2u(v[2 * j] * inv, v[2 * j + 1] * inv);
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + token * p.ot + head * p.oh + d0) =
-      make_uint4(w[0], w[1], w[2], w[3]);
-  if (p.lse && d0 == 0)
-    p.lse[token * p.q_heads + head] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
-}
-
 template <int D>
 struct Tile {
   static constexpr int kCode = kTileA * D / 2, kScale = kTileA * D / 16;      // bytes of 32 keys
@@ -211,21 +173,7 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
                                                         (long long)(rt.token0 + tok) * p.qt + head * p.qh + t * (D / 4));
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 w = src[i];
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (BF16) {
-            f[8 * i + 2 * j] = bf16lo_to_f32(x[j]);
-            f[8 * i + 2 * j + 1] = bf16hi_to_f32(x[j]);
-          } else {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-            f[8 * i + 2 * j] = v.x;
-            f[8 * i + 2 * j + 1] = v.y;
-          }
-        }
-      }
+      for (int i = 0; i < D / 32; ++i) unpack8<BF16>(src[i], f + 8 * i);
     }
     // Power of two that takes the row's largest finite magnitude to [2^14, 2^15).
     float big = 0.0f;
@@ -233,8 +181,7 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
     for (int i = 0; i < D / 4; ++i) big = fmaxf(big, fabsf(f[i]) < INFINITY ? fabsf(f[i]) : 0.0f);
     big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
     big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-    // Exponent clamped so that both 2^e and 2^-e are normal numbers.
-    const int e = big > 0.0f ? min(max(14 - (int)((__float_as_uint(big) >> 23) & 0xFF) + 127, -126), 126) : 0;
+    const int e = row_exponent(big);
     const float up = __uint_as_float((uint32_t)(127 + e) << 23);
     if (t == 0) back[r] = p.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
@@ -525,30 +472,16 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
   }
 }
 
-__device__ __forceinline__ Kv4Work work_of(const Kv4AttnLaunch& p, int tile_rows) {
-  Kv4Work w;
-  w.q_start = p.q_start;
-  w.kv_len = p.kv_len;
-  w.requests = p.requests;
-  w.tokens = p.tokens;
-  w.group = p.q_heads / p.c.heads;
-  w.heads = p.c.heads;
-  w.tile_rows = tile_rows;
-  w.causal = p.causal;
-  w.max_rows = p.max_rows;
-  w.capacity = (long long)p.max_pages << p.c.page_log2;
-  return w;
-}
-
 template <int D, int NT, bool BF16>
 __global__ void __launch_bounds__(kThreadsA, ctas_per_sm(NT))
     kv4_attention_kernel(const __grid_constant__ Kv4AttnLaunch p) {
   griddep_wait();
   griddep_launch_dependents();
-  const Kv4Work w = work_of(p, 8 * NT);
+  const Kv4Work w = work_of(p);
   const WarpUnits wu = warp_units(w);
   const long long per = (wu.total + gridDim.x - 1) / gridDim.x;
   const long long u0 = per * blockIdx.x, u1 = min(u0 + per, wu.total);
+  bool noted = false;
   for (long long u = u0; u < u1;) {
     long long first;
     const int b = request_of_unit(w, wu, u, &first);
@@ -558,48 +491,51 @@ __global__ void __launch_bounds__(kThreadsA, ctas_per_sm(NT))
     attend_segment<D, NT, BF16>(p, sg.tile, sg.head, sg.unit0 * kUnitKeys,
                                 min(sg.tile.last_key, (sg.unit0 + n) * kUnitKeys), whole,
                                 2ll * blockIdx.x + (u == u0 ? 0 : 1));
+    if (!whole && sg.unit0 == 0) {
+      if (threadIdx.x == 0) p.cuts[blockIdx.x] = cut_of(sg.tile, sg.head, (int)((u + sg.units - 1) / per), u == u0 ? 0 : 1);
+      noted = true;
+    }
     u += n;
     __syncthreads();                                      // shared memory changes hands
   }
+  if (p.join && !noted && threadIdx.x == 0) p.cuts[blockIdx.x].rows = 0;
 }
 
-// Joins the parts of segments that several CTAs took: WR warps (1 or all 8 of
-// the CTA) for one (token, head) at a time.  Warp w of them adds parts w, w +
-// WR, ..., eight in flight, and the warps' sums are added in order.  Where the
-// parts lie follows from the lengths alone, and is worked out while the first
-// kernel still runs (it lets this one start only after what precedes both has
-// ended).
+// Joins the parts of segments that several CTAs took, row by row: item (c, r)
+// is row r of the segment that CTA c began and did not finish (the first kernel
+// left a note of it).  WR warps take an item: 1, while a segment has a few
+// parts, or all 8, and then a CTA looks at 32 notes at once for the few that
+// exist.  Warp w of them adds parts w, w + WR, ..., eight in flight, and the
+// warps' sums are added in order.
 constexpr int kWarpsJ = 8;
-template <int D, int NT, int WR, bool BF16>
+template <int D, int WR, bool BF16>
 __global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_kernel(const __grid_constant__ Kv4AttnLaunch p) {
   constexpr int kVec = D / 32, kFlight = 8;               // floats a lane, parts in flight
   __shared__ float acc[kWarpsJ][D];
   __shared__ float2 sums[kWarpsJ];
-  const Kv4Work w = work_of(p, 8 * NT);
-  const WarpUnits wu = warp_units(w);
-  const long long per = (wu.total + p.ctas - 1) / p.ctas;
-  const int lane = threadIdx.x & 31, team = (threadIdx.x >> 5) / WR, warp = (threadIdx.x >> 5) % WR;
-  const long long rows = (long long)p.tokens * p.q_heads;
-  bool waited = false;
-  // (With WR = 8 all of the CTA's warps take the same rows and the same branches.)
-  for (long long i = (long long)blockIdx.x * (kWarpsJ / WR) + team; i < rows; i += (long long)gridDim.x * (kWarpsJ / WR)) {
-    const int token = (int)(i / p.q_heads), head = (int)(i - (long long)token * p.q_heads);
-    const int b = request_of(p.q_start, p.requests, p.tokens, token);
-    if (b < 0) continue;                                  // a token of no request
-    const RequestSpan s = span_of(w, b);
-    const int tok = token - s.token0;
-    if (tok < 0 || tok >= s.n) continue;                  // the request is left out here
-    const int kvh = head / w.group;
-    const long long row = (long long)tok * w.group + head % w.group;
-    int units;
-    const long long first = first_unit_of(w, wu, b) + segment_start(w, s, row, kvh, &units);
-    const int c0 = (int)(first / per), c1 = (int)((first + units - 1) / per);
-    if (c0 == c1) continue;                               // finished by its one CTA
-    const int r = (int)(row % w.tile_rows);
-    const bool late = first != c0 * per;
-    auto part_row = [&](int c) { return (2ll * c + (c == c0 && late ? 1 : 0)) * w.tile_rows + r; };
-    if (!waited) griddep_wait();
-    waited = true;
+  const int lane = threadIdx.x & 31, warp = WR == 1 ? 0 : threadIdx.x >> 5;
+  const int group = p.q_heads / p.c.heads;
+  griddep_wait();
+  griddep_launch_dependents();
+  // WR = 1: warps stride over all items.  WR = 8: block (x, r), row r of the notes 32 x .. 32 x + 31.
+  const long long items = (long long)(p.ctas - 1) * p.tile_rows, step = (long long)gridDim.x * kWarpsJ;
+  const int note = 32 * blockIdx.x + lane;
+  unsigned found = 0;
+  if (WR != 1) found = __ballot_sync(0xFFFFFFFFu, note < p.ctas && (int)blockIdx.y < p.cuts[min(note, p.ctas - 1)].rows);
+  for (long long i = (long long)blockIdx.x * kWarpsJ + (threadIdx.x >> 5); WR == 1 ? i < items : found != 0; i += step) {
+    int c0, r;
+    if (WR == 1) {
+      c0 = (int)(i / p.tile_rows);
+      r = (int)(i - (long long)c0 * p.tile_rows);
+    } else {
+      c0 = 32 * blockIdx.x + __ffs(found) - 1;
+      r = blockIdx.y;
+      found &= found - 1;
+    }
+    const Kv4Cut cut = p.cuts[c0];
+    if (r >= cut.rows) continue;
+    const int c1 = cut.last_cta;
+    auto part_row = [&](int c) { return (2ll * c + (c == c0 ? cut.slot : 0)) * p.tile_rows + r; };
     float top = -INFINITY, total = 0.0f, v[kVec];
 #pragma unroll
     for (int j = 0; j < kVec; ++j) v[j] = 0.0f;
@@ -608,16 +544,18 @@ __global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_kernel(const __grid_con
       float a[kFlight][kVec];
 #pragma unroll
       for (int q = 0; q < kFlight; ++q) {
-        const bool there = c + WR * q <= c1;
-        const long long at = part_row(there ? c + WR * q : c);
-        const float* src = p.part_o + at * D + kVec * lane;
-        ml[q] = there ? p.part_ml[at] : make_float2(-INFINITY, 0.0f);
-        if (kVec == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(src);
-          a[q][0] = x.x, a[q][1] = x.y, a[q][kVec - 2] = x.z, a[q][kVec - 1] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(src);
-          a[q][0] = x.x, a[q][1] = x.y;
+        ml[q] = make_float2(-INFINITY, 0.0f);
+        if (c + WR * q <= c1) {
+          const long long at = part_row(c + WR * q);
+          const float* src = p.part_o + at * D + kVec * lane;
+          ml[q] = p.part_ml[at];
+          if (kVec == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            a[q][0] = x.x, a[q][1] = x.y, a[q][kVec - 2] = x.z, a[q][kVec - 1] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            a[q][0] = x.x, a[q][1] = x.y;
+          }
         }
       }
       float to = top;
@@ -638,6 +576,8 @@ __global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_kernel(const __grid_con
         }
       }
     }
+    const int row = cut.row0 + r, tok = row / group, head = cut.head * group + row - tok * group;
+    const long long token = cut.token0 + tok;
     const int wj = threadIdx.x >> 5;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) acc[wj][kVec * lane + j] = v[j];
@@ -673,34 +613,14 @@ __global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_kernel(const __grid_con
     }
     __syncthreads();
   }
-  // Every CTA waits, so that this kernel's end implies the first one's.
-  if (!waited) griddep_wait();
-  griddep_launch_dependents();
 }
 
-int tile_rows_for(const Kv4AttnLaunch& p) {
-  const int group = p.q_heads / p.c.heads;
-  // The smallest tile that holds an average request's rows: a larger one
-  // dequantizes each key for more rows at once, a smaller one leaves room for
-  // more warps.
-  const long long rows = (long long)p.tokens * group;
-  return rows <= 8ll * p.requests ? 8 : rows <= 16ll * p.requests ? 16 : 32;
-}
+// Requests of at most kFewRows rows (query heads of one key head x tokens) go to
+// this file's kernel, larger ones to kv4_attention_tc.cu.
+constexpr int kFewRows = 64, kFewRowsInAll = 512;
 
-template <typename... Args>
-cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                         const Kv4AttnLaunch& p) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+size_t parts_bytes(const Kv4AttnLaunch& p) {
+  return p.join ? (size_t)p.ctas * (2 * p.tile_rows * ((size_t)p.c.D * 4 + 8) + sizeof(Kv4Cut)) : 0;
 }
 
 template <int D, int NT, bool BF16>
@@ -708,51 +628,93 @@ cudaError_t launch_nt(const Kv4AttnLaunch& p, cudaStream_t stream) {
   constexpr int kSmem = smem_bytes<D, NT>();
   cudaError_t e = ensure_smem_limit(kv4_attention_kernel<D, NT, BF16>, kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_after(kv4_attention_kernel<D, NT, BF16>, dim3((unsigned)p.ctas), kThreadsA, kSmem, stream, p);
-  if (e != cudaSuccess || !p.join) return e;
-  const long long rows = (long long)p.tokens * p.q_heads;
-  // A warp a row while a row has a few parts, eight for the many parts of few long sequences.
-  const bool many = p.ctas > 8 * p.segments;
-  const long long teams = many ? rows : (rows + kWarpsJ - 1) / kWarpsJ, most = 8ll * p.num_sms;
-  const dim3 grid((unsigned)(teams < most ? teams : most));
-  return many ? launch_after(kv4_join_kernel<D, NT, kWarpsJ, BF16>, grid, 32 * kWarpsJ, 0, stream, p)
-              : launch_after(kv4_join_kernel<D, NT, 1, BF16>, grid, 32 * kWarpsJ, 0, stream, p);
+  return launch_after(kv4_attention_kernel<D, NT, BF16>, dim3((unsigned)p.ctas), kThreadsA, kSmem, stream, p);
 }
-
 template <int D, bool BF16>
-cudaError_t launch_d(const Kv4AttnLaunch& p, cudaStream_t stream) {
+cudaError_t launch_few(const Kv4AttnLaunch& p, cudaStream_t stream) {
   if (p.tile_rows == 8) return launch_nt<D, 1, BF16>(p, stream);
   if (p.tile_rows == 16) return launch_nt<D, 2, BF16>(p, stream);
   return launch_nt<D, 4, BF16>(p, stream);
 }
+template <int D, bool BF16>
+cudaError_t launch_join(const Kv4AttnLaunch& p, cudaStream_t stream) {
+  if (p.ctas > 8 * p.segments)
+    return launch_after(kv4_join_kernel<D, kWarpsJ, BF16>, dim3((unsigned)(p.ctas + 31) / 32, (unsigned)p.tile_rows),
+                        32 * kWarpsJ, 0, stream, p);
+  const long long blocks = ((long long)(p.ctas - 1) * p.tile_rows + kWarpsJ - 1) / kWarpsJ, most = 16ll * p.num_sms;
+  return launch_after(kv4_join_kernel<D, 1, BF16>, dim3((unsigned)(blocks < most ? blocks : most)), 32 * kWarpsJ, 0, stream, p);
+}
+template <int D, bool BF16>
+cudaError_t launch_all(const Kv4Plan& plan, uint8_t* workspace, cudaStream_t stream) {
+  const Kv4AttnLaunch* launches[2] = {plan.use_few ? &plan.few : nullptr, plan.use_many ? &plan.many : nullptr};
+  for (int i = 0; i < 2; ++i) {
+    if (!launches[i]) continue;
+    Kv4AttnLaunch p = *launches[i];
+    if (p.join) {
+      p.part_o = reinterpret_cast<float*>(workspace);
+      p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)p.ctas * 2 * p.tile_rows * D);
+      p.cuts = reinterpret_cast<Kv4Cut*>(p.part_ml + (size_t)p.ctas * 2 * p.tile_rows);
+      workspace += parts_bytes(p);
+    }
+    cudaError_t e = i == 0 ? launch_few<D, BF16>(p, stream) : launch_kv4_attention_tc(p, stream);
+    if (e == cudaSuccess && p.join) e = launch_join<D, BF16>(p, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
-}  // namespace
-
-void kv4_attention_plan(Kv4AttnLaunch& p, int max_kv, int num_sms) {
-  p.num_sms = num_sms;
-  p.tile_rows = tile_rows_for(p);
-  p.max_rows = 0x7FFFFFFF;
-  // One resident set of CTAs shares the
-  // work evenly, whatever the lengths; no more CTAs than units of work.
-  p.segments = max_units(p.tokens, p.requests, p.q_heads / p.c.heads, p.c.heads, p.tile_rows, p.q_start != nullptr, 0);
+// Fills in the launch for requests of min_rows .. max_rows rows, in tiles of tile_rows.
+void plan_launch(Kv4AttnLaunch& p, int tile_rows, int min_rows, int max_rows, long long slots, int max_kv) {
+  p.tile_rows = tile_rows;
+  p.min_rows = min_rows;
+  p.max_rows = max_rows;
+  // One resident set of CTAs shares the work evenly, whatever the lengths; no
+  // more CTAs than units of work.
+  p.segments = max_units(p.tokens, p.requests, p.q_heads / p.c.heads, p.c.heads, tile_rows, p.q_start != nullptr, 0);
   const long long units = p.segments * tile_units(max_kv);
-  const long long slots = (long long)num_sms * ctas_per_sm(p.tile_rows / 8);
   p.ctas = (int)(units < slots ? (units > 0 ? units : 1) : slots);
   // One CTA, or tables that hold one unit at most: no segment is ever cut.
   p.join = p.ctas > 1 && ((long long)p.max_pages << p.c.page_log2) > kUnitKeys;
 }
 
-size_t kv4_attention_workspace(const Kv4AttnLaunch& p) {
-  return p.join ? (size_t)p.ctas * 2 * p.tile_rows * ((size_t)p.c.D * 4 + 8) : 0;
+}  // namespace
+
+Kv4Plan kv4_attention_plan(const Kv4AttnLaunch& base, int max_kv, int num_sms) {
+  Kv4Plan plan;
+  plan.few = plan.many = base;
+  plan.few.num_sms = plan.many.num_sms = num_sms;
+  const long long rows = (long long)base.tokens * (base.q_heads / base.c.heads);
+  constexpr int kAll = 0x7FFFFFFF;
+  if (!base.q_start) {
+    plan.use_many = rows > (long long)kFewRows * base.requests;
+    plan.use_few = !plan.use_many;
+  } else {
+    // The requests' sizes are on the device: each kernel takes its own.  A few
+    // hundred rows in all are left to the one kernel, and where requests have
+    // 256 rows on average all of them to the other: small requests among them
+    // take no more of its tiles than the large ones.
+    plan.use_many = rows > kFewRowsInAll;
+    plan.use_few = rows < 256ll * base.requests;
+  }
+  // The smallest tile that holds an average request's rows: a larger one
+  // dequantizes each key for more rows at once, a smaller one leaves room for
+  // more warps.
+  const long long share = plan.use_many && plan.use_few ? kFewRows : rows;
+  const int nt = share <= 8ll * base.requests ? 1 : share <= 16ll * base.requests ? 2 : 4;
+  plan_launch(plan.few, 8 * nt, 0, plan.use_many ? kFewRows : kAll, (long long)num_sms * ctas_per_sm(nt), max_kv);
+  plan_launch(plan.many, 256, plan.use_few ? kFewRows + 1 : 0, kAll, num_sms, max_kv);
+  return plan;
 }
 
-cudaError_t launch_kv4_attention(const Kv4AttnLaunch& p0, void* workspace, cudaStream_t stream) {
-  Kv4AttnLaunch p = p0;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_ml = p.join ? reinterpret_cast<float2*>(p.part_o + (size_t)p.ctas * 2 * p.tile_rows * p.c.D) : nullptr;
-  if (p.c.D == 128)
-    return p.dtype == 0 ? launch_d<128, true>(p, stream) : launch_d<128, false>(p, stream);
-  return p.dtype == 0 ? launch_d<64, true>(p, stream) : launch_d<64, false>(p, stream);
+size_t kv4_attention_workspace(const Kv4Plan& plan) {
+  return (plan.use_few ? parts_bytes(plan.few) : 0) + (plan.use_many ? parts_bytes(plan.many) : 0);
+}
+
+cudaError_t launch_kv4_attention(const Kv4Plan& plan, void* workspace, cudaStream_t stream) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const Kv4AttnLaunch& p = plan.few;
+  if (p.c.D == 128) return p.dtype == 0 ? launch_all<128, true>(plan, ws, stream) : launch_all<128, false>(plan, ws, stream);
+  return p.dtype == 0 ? launch_all<64, true>(plan, ws, stream) : launch_all<64, false>(plan, ws, stream);
 }
 
 }  // namespace svdq

@@ -70,28 +70,53 @@ KV4_HD RowTile tile_of(const RequestSpan& s, int b, int group, int tile_rows, lo
 // c takes units c * per .. (c + 1) * per.  A segment that lies in one share is
 // finished there; otherwise each of its CTAs leaves a part, in slot 0 if the
 // segment covers the share's first unit and in slot 1 if it starts later (at
-// most one of each a CTA).
+// most one of each a CTA).  A CTA begins at most one segment that it does not
+// finish, the last of its share.
 constexpr int kUnitKeys = 128;
 struct Kv4Work {
   const int *q_start, *kv_len;
   int requests, tokens, group, heads, tile_rows, causal;
-  int max_rows;                                 // requests with more rows are left out
+  int min_rows, max_rows;                       // requests with fewer or more rows are left out
   long long capacity;                           // keys that a block table can hold
 };
 KV4_HD RequestSpan span_of(const Kv4Work& w, int b) {
   RequestSpan s = request_span(w.q_start, w.kv_len, w.requests, w.tokens, b, w.capacity);
-  if ((long long)s.n * w.group > w.max_rows) s.n = 0;
+  const long long rows = (long long)s.n * w.group;
+  if (rows < w.min_rows || rows > w.max_rows) s.n = 0;
   return s;
 }
 KV4_HD int tile_units(int last_key) { return last_key > 0 ? (last_key - 1) / kUnitKeys + 1 : 1; }
 KV4_HD int tiles_of(const Kv4Work& w, const RequestSpan& s) {
   return (int)(((long long)s.n * w.group + w.tile_rows - 1) / w.tile_rows);
 }
+// Steps through a request's tiles: the token of each tile's last row, without
+// a division a tile.
+struct TileWalk {
+  int tok, rem, more_tok, more_rem, group, last;
+  KV4_HD TileWalk(const Kv4Work& w, const RequestSpan& s)
+      : tok((w.tile_rows - 1) / w.group),
+        rem((w.tile_rows - 1) % w.group),
+        more_tok(w.tile_rows / w.group),
+        more_rem(w.tile_rows % w.group),
+        group(w.group),
+        last(s.n - 1) {}
+  KV4_HD int last_token() const { return tok < last ? tok : last; }
+  KV4_HD void next() {
+    tok += more_tok;
+    rem += more_rem;
+    if (rem >= group) {
+      rem -= group;
+      ++tok;
+    }
+  }
+};
 // Units of a request under one head.
 KV4_HD long long head_units(const Kv4Work& w, const RequestSpan& s) {
   const int nt = tiles_of(w, s);
+  if (!w.causal) return (long long)nt * tile_units(s.keys);
+  TileWalk walk(w, s);
   long long u = 0;
-  for (int t = 0; t < nt; ++t) u += tile_units(tile_of(s, 0, w.group, w.tile_rows, t, w.causal).last_key);
+  for (int t = 0; t < nt; ++t, walk.next()) u += tile_units(keys_seen(s.keys, s.n, walk.last_token(), 1));
   return u;
 }
 struct Segment {
@@ -104,42 +129,22 @@ KV4_HD Segment segment_in(const Kv4Work& w, const RequestSpan& s, int b, long lo
   Segment g;
   g.head = (int)(u / per_head);
   u -= g.head * per_head;
-  for (int t = 0;; ++t) {
-    g.tile = tile_of(s, b, w.group, w.tile_rows, t, w.causal);
-    g.units = tile_units(g.tile.last_key);
-    if (u < g.units) break;
-    u -= g.units;
+  int t = 0;
+  if (!w.causal) {
+    g.units = tile_units(s.keys);
+    t = (int)(u / g.units);
+    u -= (long long)t * g.units;
+  } else {
+    TileWalk walk(w, s);
+    for (;; ++t, walk.next()) {
+      g.units = tile_units(keys_seen(s.keys, s.n, walk.last_token(), 1));
+      if (u < g.units) break;
+      u -= g.units;
+    }
   }
+  g.tile = tile_of(s, b, w.group, w.tile_rows, t, w.causal);
   g.unit0 = (int)u;
   return g;
-}
-// First unit of the segment that holds row `row` of request b under `head`, from the request's first unit.
-KV4_HD long long segment_start(const Kv4Work& w, const RequestSpan& s, long long row, int head, int* units) {
-  const int tile = (int)(row / w.tile_rows);
-  long long u = head * head_units(w, s);
-  for (int t = 0; t < tile; ++t) u += tile_units(tile_of(s, 0, w.group, w.tile_rows, t, w.causal).last_key);
-  *units = tile_units(tile_of(s, 0, w.group, w.tile_rows, tile, w.causal).last_key);
-  return u;
-}
-// The request that holds query token `token`, or -1.
-KV4_HD int request_of(const int* q_start, int requests, int tokens, int token) {
-  int b;
-  if (q_start) {
-    // The last request that starts at or before the token (starts ascend).
-    int lo = 0, hi = requests;
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (q_start[mid] <= token) lo = mid + 1;
-      else hi = mid;
-    }
-    b = lo - 1;
-  } else {
-    const int n = tokens / requests;
-    b = n > 0 ? token / n : -1;
-  }
-  if (b < 0 || b >= requests) return -1;
-  const RequestSpan s = request_span(q_start, nullptr, requests, tokens, b, 0);
-  return token >= s.token0 && token < s.token0 + s.n ? b : -1;
 }
 // Upper bound of the units of a launch whose requests have at most `max_kv` keys.
 KV4_HD long long max_units(int tokens, int requests, int group, int heads, int tile_rows, bool ragged, int max_kv) {
@@ -195,16 +200,6 @@ __device__ __forceinline__ int request_of_unit(const Kv4Work& w, const WarpUnits
   }
   *first = before;
   return w.requests - 1;
-}
-// First unit of request b.
-__device__ __forceinline__ long long first_unit_of(const Kv4Work& w, const WarpUnits& r, int b) {
-  const int lane = threadIdx.x & 31;
-  long long before = 0;
-  for (int b0 = 0; b0 + 31 < b; b0 += 32) before += __shfl_sync(0xFFFFFFFFu, warp_prefix(units_of_request(w, b0 + lane)), 31);
-  const int b0 = b & ~31;
-  const long long mine = w.requests <= 32 ? r.mine : units_of_request(w, b0 + lane);
-  const long long upto = w.requests <= 32 ? r.upto : warp_prefix(mine);
-  return before + __shfl_sync(0xFFFFFFFFu, upto - mine, b & 31);
 }
 #endif
 

@@ -132,6 +132,14 @@ SVDQ_API size_t svdq_kv4_attention_workspace_bytes(const svdq_kv4_attention_desc
 SVDQ_API svdq_status svdq_kv4_attention(const svdq_kv4_attention_desc* desc, void* workspace, size_t workspace_bytes,
                                         void* stream);
 
+/*
+ * svdq_kv4_attention_status -- synchronize the current device and read + clear
+ * the error word of svdq_kv4_attention's tensor-core kernel there (nonzero when
+ * a bounded wait expired: the kernel then skipped its remaining work).  Returns
+ * SVDQ_ERR_DEVICE when it was nonzero.
+ */
+SVDQ_API svdq_status svdq_kv4_attention_status(int* flags);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,9 +38,10 @@ int main() {
     w.requests = pick(1, 40);
     w.group = pick(1, 9);
     w.heads = pick(1, 4);
-    w.tile_rows = pick(0, 1) ? 16 : 32;
+    w.tile_rows = 8 << pick(0, 5);
     w.causal = pick(0, 1);
-    w.max_rows = pick(0, 2) ? 0x7FFFFFFF : pick(1, 100);
+    w.min_rows = pick(0, 2) ? 0 : pick(1, 50);
+    w.max_rows = pick(0, 2) ? 0x7FFFFFFF : w.min_rows + pick(0, 100);
     const bool ragged = pick(0, 3) != 0;
     const int page = 16 << pick(0, 4), max_pages = pick(0, 6);
     w.capacity = (long long)page * max_pages;
@@ -52,7 +53,6 @@ int main() {
       start[b + 1] = tokens;
       len[b] = pick(0, 9) == 0 ? pick(-5, 5) : pick(0, (int)w.capacity + 20);
     }
-    const int behind = tokens;
     tokens += pick(0, 3);                                // and behind the last
     if (!ragged) tokens = per_request * w.requests;
     w.tokens = tokens;
@@ -60,13 +60,16 @@ int main() {
     w.kv_len = len.data();
 
     const long long total = total_units(w);
-    if (w.max_rows == 0x7FFFFFFF)
-      CHECK(total <= max_units(tokens, w.requests, w.group, w.heads, w.tile_rows, ragged, (int)w.capacity));
+    CHECK(total <= max_units(tokens, w.requests, w.group, w.heads, w.tile_rows, ragged, (int)w.capacity));
     const int ctas = pick(1, 50);
     const long long per = (total + ctas - 1) / ctas;
     // (token, query head) -> keys taken so far; parts by slot.
     std::map<std::pair<int, int>, int> taken;
     std::map<long long, std::vector<std::pair<int, int>>> slots;
+    struct Cut {
+      int token0, row0, rows, head, last_cta, slot;
+    };
+    std::vector<Cut> cuts(ctas, Cut{0, 0, 0, 0, 0, 0});
     for (int c = 0; c < ctas; ++c) {
       const long long u0 = per * c, u1 = u0 + per < total ? u0 + per : total;
       for (long long u = u0; u < u1;) {
@@ -83,6 +86,10 @@ int main() {
         const bool whole = n == g.units;
         const long long part = 2ll * c + (u == u0 ? 0 : 1);
         if (!whole) CHECK(slots.find(part) == slots.end());
+        if (!whole && g.unit0 == 0) {
+          CHECK(cuts[c].rows == 0 && u + n == u1);
+          cuts[c] = Cut{g.tile.token0, g.tile.row0, g.tile.rows, g.head, (int)((u + g.units - 1) / per), u == u0 ? 0 : 1};
+        }
         for (int i = 0; i < g.tile.rows; ++i) {
           const int row = g.tile.row0 + i, tok = row / w.group, head = g.head * w.group + row % w.group;
           CHECK(tok < g.tile.n && g.tile.token0 + tok < tokens);
@@ -95,32 +102,33 @@ int main() {
         u += n;
       }
     }
-    // The joining kernel's view of every row.
-    for (int t = 0; t < tokens; ++t)
-      for (int head = 0; head < w.group * w.heads; ++head) {
-        const auto key = std::make_pair(t, head);
-        const int b = request_of(w.q_start, w.requests, tokens, t);
-        CHECK((b >= 0) == (!ragged || (t >= start[0] && t < behind)));
-        if (b < 0 || t - span_of(w, b).token0 >= span_of(w, b).n) {
-          CHECK(taken.find(key) == taken.end());
-          continue;
+    // Every row of the requests that take part has all its keys.
+    for (int b = 0; b < w.requests; ++b) {
+      const RequestSpan s = span_of(w, b);
+      for (int i = 0; i < s.n; ++i)
+        for (int head = 0; head < w.group * w.heads; ++head) {
+          const long long row = (long long)i * w.group + head % w.group;
+          const auto key = std::make_pair(s.token0 + i, head);
+          CHECK(taken.count(key) && taken[key] == tile_of(s, b, w.group, w.tile_rows, row / w.tile_rows, w.causal).last_key);
+          taken.erase(key);
         }
-        const RequestSpan s = span_of(w, b);
-        const long long row = (long long)(t - s.token0) * w.group + head % w.group;
-        const RowTile rt = tile_of(s, b, w.group, w.tile_rows, row / w.tile_rows, w.causal);
-        CHECK(taken.count(key) && taken[key] == rt.last_key);
-        int units;
-        long long first = segment_start(w, s, row, head / w.group, &units);
-        for (int i = 0; i < b; ++i) first += units_of(w, i);
-        CHECK(units == tile_units(rt.last_key) && first + units <= total);
-        const int c0 = (int)(first / per), c1 = (int)((first + units - 1) / per);
-        CHECK(c1 < ctas);
-        for (int c = c0; c <= c1 && c0 != c1; ++c) {
-          const long long part = 2ll * c + (c == c0 && first != c0 * per ? 1 : 0);
-          const auto& rows = slots[part];
-          CHECK((int)rows.size() > (int)(row % w.tile_rows) && rows[row % w.tile_rows] == key);
+    }
+    CHECK(taken.empty());
+    // The joining kernel's view: each cut segment from the note of the CTA that began it, its parts where they were left.
+    std::set<long long> joined;
+    for (int c0 = 0; c0 < ctas; ++c0) {
+      if (!cuts[c0].rows) continue;
+      for (int c = c0; c <= cuts[c0].last_cta; ++c) {
+        const long long part = 2ll * c + (c == c0 ? cuts[c0].slot : 0);
+        CHECK(c < ctas && joined.insert(part).second && (int)slots[part].size() == cuts[c0].rows);
+        for (int i = 0; i < cuts[c0].rows; ++i) {
+          const int row = cuts[c0].row0 + i;
+          CHECK(slots[part][i] == std::make_pair(cuts[c0].token0 + row / w.group, cuts[c0].head * w.group + row % w.group));
         }
       }
+    }
+    CHECK(cuts[ctas - 1].rows == 0);
+    CHECK(joined.size() == slots.size());
     // Arbitrary content: nothing out of range, whatever the order of the starts.
     for (auto& v : start) v = (int)rng();
     for (auto& v : len) v = (int)rng();
@@ -133,10 +141,6 @@ int main() {
         CHECK(g.head < w.heads && g.tile.last_key <= w.capacity && g.unit0 < g.units);
         CHECK(g.tile.token0 + (g.tile.row0 + g.tile.rows - 1) / w.group < tokens);
       }
-    }
-    for (int t = 0; t < tokens; ++t) {
-      const int b = request_of(w.q_start, w.requests, tokens, t);
-      CHECK(b >= -1 && b < w.requests);
     }
   }
   std::printf("ok\n");

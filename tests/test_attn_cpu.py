@@ -25,7 +25,7 @@ def test_header_entry_points_are_exported(lib):
     with open(os.path.join(ROOT, "include", "svdq_attn.h")) as f:
         names = set(re.findall(r"SVDQ_API\s+[\w\s\*]+?\b(svdq_\w+)\s*\(", f.read()))
     assert names == {"svdq_qk_norm_rope", "svdq_kv4_append", "svdq_kv4_read", "svdq_kv4_attention_workspace_bytes",
-                     "svdq_kv4_attention"}
+                     "svdq_kv4_attention", "svdq_kv4_attention_status"}
     for n in names:
         assert hasattr(lib, n) and callable(getattr(S, n))
 
@@ -144,6 +144,7 @@ def test_attention_argument_errors(lib, kw, status):
     assert lib.svdq_kv4_attention(ctypes.addressof(_attn(**kw)), 256, 1 << 40, None) == status
     assert lib.svdq_kv4_attention(None, None, 0, None) == 1
     assert lib.svdq_kv4_attention_workspace_bytes(None) == 0
+    assert lib.svdq_kv4_attention_status(None) == 1
 
 
 def test_attention_workspace_is_checked(lib):

@@ -375,6 +375,9 @@ ATTEND = [
     ([140], 200, 2, 1, 128, 32, False, BF),                        # more queries than keys, no order
     ([1500], 130, 9, 3, 128, 64, True, FP),
     ([513], 300, 8, 1, 64, 16, True, BF),
+    ([900, 31, 400, 65], [0, 200, 201, 401, 402], 6, 2, 128, 32, True, BF),   # prompts beside single tokens
+    ([900, 31, 400, 65], [3, 300, 301, 310, 311], 4, 2, 64, 16, False, FP),
+    ([260, 0, 129], [0, 129, 400, 700], 2, 1, 128, 16, True, FP),  # a prompt without keys; more queries than keys
 ]
 
 
@@ -398,6 +401,8 @@ def test_attention(case):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1].nan_to_num(), b[1].nan_to_num())
     check(q, cache, lens, table, start, causal, max_kv_len=max(1, max(lens) // 3))
     check(q, cache, lens, table, start, causal, scale=0.31, max_kv_len=max(1, max(lens)))
+    check(q, cache, lens, table, start, causal, scale=-0.2)
+    assert S.svdq_kv4_attention_status() == 0
 
 
 def test_attention_strided_arguments():
