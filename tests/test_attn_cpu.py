@@ -47,6 +47,12 @@ def test_structures_match_the_header(tmp_path):
     for n in names:
         want += [getattr(getattr(S, n), f).offset for f, *_ in getattr(S, n)._fields_]
     assert got == want
+    from bit_quantized_linear_svdq_b200 import attention as A
+    for packed, n in ((A._HEADS, "svdq_heads"), (A._ROPE, "svdq_qk_norm_rope_desc"), (A._CACHE, "svdq_kv4_cache"),
+                      (A._ATTENTION, "svdq_kv4_attention_desc")):
+        assert packed.size == ctypes.sizeof(getattr(S, n))
+    fields = iter(range(1, 100))
+    assert bytes(S.svdq_kv4_cache(*[next(fields) for _ in range(8)])) == A._CACHE.pack(*range(1, 9))
 
 
 def test_rows_and_keys_of_the_tiles(tmp_path):
