@@ -82,7 +82,8 @@ svdq_status check_rows(const svdq_kv4_cache* cache, const svdq_heads* k, const s
   if (tokens == 0) return SVDQ_OK;
   if ((s = check_heads(*k)) != SVDQ_OK || (s = check_heads(*v)) != SVDQ_OK) return s;
   if (!slots || !aligned(slots, 8)) return fail(SVDQ_ERR_INVALID_ARG, "slots null or misaligned");
-  if ((long long)tokens * p->c.heads * 16 / 256 > kMaxBlocks) return fail(SVDQ_ERR_SHAPE, "too many tokens");
+  if ((long long)tokens * p->c.heads > kMaxBlocks / 8) return fail(SVDQ_ERR_SHAPE, "too many tokens");
+  p->num_sms = num_sms();
   p->kt = k->token_stride;
   p->kh = k->head_stride;
   p->vt = v->token_stride;
@@ -160,10 +161,16 @@ svdq_status svdq_qk_norm_rope(const svdq_qk_norm_rope_desc* d, void* stream) {
   if (d->pairs > 0 && (!d->positions || !d->inv_freq || d->axes < 1 || !aligned(d->positions, 4) || !aligned(d->inv_freq, 4)))
     return fail(SVDQ_ERR_INVALID_ARG, "positions, inv_freq and axes >= 1 are needed with pairs");
   svdq::QkNormRopeLaunch p;
-  p.q = {d->q.data, d->q_out.data, d->q_weight, d->q.token_stride, d->q.head_stride, d->q_out.token_stride,
-         d->q_out.head_stride, d->q_heads};
-  p.k = {d->k.data, d->k_out.data, d->k_weight, d->k.token_stride, d->k.head_stride, d->k_out.token_stride,
-         d->k_out.head_stride, d->k_heads};
+  const svdq_heads* sides[4] = {&d->q, &d->q_out, &d->k, &d->k_out};
+  for (int i = 0; i < 4; ++i)
+    if (i < 2 ? d->q_heads : d->k_heads)
+      if (sides[i]->token_stride != (int)sides[i]->token_stride || sides[i]->head_stride != (int)sides[i]->head_stride)
+        return fail(SVDQ_ERR_SHAPE, "strides have to fit 32 bits");
+  p.q = {d->q.data, d->q_out.data, d->q_weight, (int)d->q.token_stride, (int)d->q.head_stride,
+         (int)d->q_out.token_stride, (int)d->q_out.head_stride, d->q_heads};
+  p.k = {d->k.data, d->k_out.data, d->k_weight, (int)d->k.token_stride, (int)d->k.head_stride,
+         (int)d->k_out.token_stride, (int)d->k_out.head_stride, d->k_heads};
+  p.num_sms = num_sms();
   p.positions = d->positions;
   p.inv_freq = d->inv_freq;
   p.pair_axis = d->pair_axis;

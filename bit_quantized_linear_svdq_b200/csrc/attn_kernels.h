@@ -15,7 +15,7 @@ struct HeadSide {
   const void* x;
   void* y;
   const void* weight;             // (D) in the storage type, or null: no norm
-  long long xt, xh, yt, yh;       // token and head strides in elements
+  int xt, xh, yt, yh;             // token and head strides in elements
   int heads;
 };
 struct QkNormRopeLaunch {
@@ -24,7 +24,7 @@ struct QkNormRopeLaunch {
   const float* inv_freq;          // (pairs)
   const uint8_t* pair_axis;       // (pairs) or null: axis 0
   long long pos_stride;
-  int tokens, D, dtype, axes, pairs;
+  int tokens, D, dtype, axes, pairs, num_sms;
   float eps;
   bool interleaved, hadamard;
 };
@@ -44,7 +44,7 @@ struct Kv4RowsLaunch {
   void *k_out, *v_out;            // read: outputs
   long long kt, kh, vt, vh;       // token and head strides of k / v (or k_out / v_out), elements
   const long long* slots;         // (tokens); page * page_size + offset, outside the cache: skipped / zeros
-  int tokens, dtype;
+  int tokens, dtype, num_sms;
 };
 cudaError_t launch_kv4_append(const Kv4RowsLaunch& p, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4RowsLaunch& p, cudaStream_t stream);

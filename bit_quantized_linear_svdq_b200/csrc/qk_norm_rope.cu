@@ -31,42 +31,55 @@
 
 #include "attn_kernels.h"
 #include "hadamard.cuh"
+#include "kcommon.cuh"
 #include "ptx.cuh"
 
 namespace svdq {
 namespace {
 
 constexpr int kThreadsR = 256;
-constexpr int kMaxTable = 2048;                 // cos/sin pairs per CTA (16 KB)
+constexpr int kCtasR = 4;                       // resident CTAs an SM (64 registers)
+constexpr int kMaxTable = 4096;                 // cos/sin pairs per CTA (32 KB)
 
+// One 16-byte chunk <-> four packed fp32 pairs.
 template <bool BF16>
-__device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
+__device__ __forceinline__ void unpack4(uint4 w, uint64_t (&v)[4]) {
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (BF16) {
-      v[2 * i] = bf16lo_to_f32(x[i]);
-      v[2 * i + 1] = bf16hi_to_f32(x[i]);
+      v[i] = pk2(bf16lo_to_f32(x[i]), bf16hi_to_f32(x[i]));
     } else {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
+      v[i] = pk2(f.x, f.y);
     }
   }
 }
 template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+__device__ __forceinline__ uint4 pack4(const uint64_t (&v)[4]) {
   uint32_t x[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (BF16) {
-      x[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      x[i] = pack_bf16x2(lo2(v[i]), hi2(v[i]));
     } else {
-      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      const __half2 h = __floats2half2_rn(lo2(v[i]), hi2(v[i]));
       x[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
   return make_uint4(x[0], x[1], x[2], x[3]);
+}
+// Four consecutive floats of shared memory as two pairs.
+__device__ __forceinline__ void load2(const float* p, uint64_t& a, uint64_t& b) {
+  const float4 f = *reinterpret_cast<const float4*>(p);
+  a = pk2(f.x, f.y);
+  b = pk2(f.z, f.w);
+}
+
+// (a, b) <- (a cos - b sin, a sin + b cos)
+__device__ __forceinline__ void turn(uint64_t& v, float cs, float sn) {
+  const float a = lo2(v), b = hi2(v);
+  v = pk2(fmaf(a, cs, -(b * sn)), fmaf(a, sn, b * cs));
 }
 
 struct RowsArgs {
@@ -76,118 +89,148 @@ struct RowsArgs {
 
 // BF16: storage type.  LOGLP: log2 of the lanes per row.
 template <bool BF16, int LOGLP>
-__global__ void __launch_bounds__(kThreadsR) qk_norm_rope_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(kThreadsR, kCtasR) qk_norm_rope_kernel(const __grid_constant__ RowsArgs a) {
   constexpr int LP = 1 << LOGLP, kSlots = kThreadsR / LP;
-  __shared__ float2 cs[kMaxTable];
+  // Of token t and pair j: cos and sin, adjacent for adjacent pairs, in two halves of the table otherwise.
+  __shared__ __align__(16) float table[2 * kMaxTable];
+  __shared__ __align__(16) float gain[2][16 * LP];        // norm weights of queries and keys
   const QkNormRopeLaunch& p = a.p;
-  const int D = p.D, P = p.pairs, heads = p.q.heads + p.k.heads;
+  const int D = p.D, P = p.pairs, chunks = D / 8;
   const int t0 = blockIdx.x * a.tb, nt = min(a.tb, p.tokens - t0);
-  const int h0 = blockIdx.y * a.hb, nh = min(a.hb, heads - h0);
   const int slot = threadIdx.x / LP, l = threadIdx.x % LP;
-  const int chunks = D / 8, rows = nt * nh;
+  const bool inter = p.interleaved, whole = chunks == 2 * LP && 2 * P == D;       // every lane full, every pair rotated
+  const float inv_d = 1.0f / (float)D;
 
-  // Row r of this CTA: its token, whether it is a key, its first element.
-  auto load = [&](int r, uint4 (&w)[2]) {
-    w[0] = w[1] = make_uint4(0, 0, 0, 0);
-    if (r >= rows) return;
-    const int t = t0 + r / nh;
-    int h = h0 + r % nh;
-    const bool key = h >= p.q.heads;
-    const HeadSide& s = key ? p.k : p.q;
-    if (key) h -= p.q.heads;
-    const uint16_t* x = static_cast<const uint16_t*>(s.x) + t * s.xt + h * s.xh;
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-      if (l + LP * c < chunks) w[c] = *reinterpret_cast<const uint4*>(x + 8 * (l + LP * c));
-  };
-
-  uint4 w[2], wn[2];
-  load(slot, w);
-  for (int i = threadIdx.x; i < nt * P; i += kThreadsR) {
-    const int t = i / P, j = i - t * P;
-    const int ax = p.pair_axis ? min((int)p.pair_axis[j], p.axes - 1) : 0;
-    const int pos = p.positions[(t0 + t) * p.pos_stride + ax];
-    double turn = (double)pos * (double)p.inv_freq[j] * 0.15915494309189535;      // 1 / 2pi
-    turn -= rint(turn);
-    float sn, cn;
-    sincospif(2.0f * (float)turn, &sn, &cn);
-    cs[i] = make_float2(cn, sn);
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int i = threadIdx.x; i < 2 * D; i += kThreadsR) {
+    const uint16_t* g = static_cast<const uint16_t*>(i < D ? p.q.weight : p.k.weight);
+    if (g) {
+      const uint16_t bits = g[i < D ? i : i - D];
+      gain[i >= D][i < D ? i : i - D] =
+          BF16 ? __uint_as_float((uint32_t)bits << 16) : __half2float(__ushort_as_half(bits));
+    }
   }
-  __syncthreads();
+  bool filled = false;
+  for (int side = 0; side < 2; ++side) {                  // the same for the whole CTA
+    const HeadSide& s = side ? p.k : p.q;
+    const int off = side ? p.q.heads : 0;
+    const int first = max((int)blockIdx.y * a.hb - off, 0), nh = min((int)(blockIdx.y + 1) * a.hb - off, s.heads) - first;
+    if (nh <= 0) continue;
+    // Row r = (token, head) of this side; a slot's next row is kSlots further.
+    const int rows = nt * nh, more_t = kSlots / nh, more_h = kSlots % nh;
+    int t = slot / nh, h = slot - t * nh, tn = t, hn = h;
+    auto advance = [&](int& tt, int& hh) {
+      tt += more_t;
+      hh += more_h;
+      if (hh >= nh) {
+        hh -= nh;
+        ++tt;
+      }
+    };
+    const uint16_t* x0 = static_cast<const uint16_t*>(s.x) + (long long)t0 * s.xt + (long long)first * s.xh + 8 * l;
+    uint16_t* y0 = static_cast<uint16_t*>(s.y) + (long long)t0 * s.yt + (long long)first * s.yh + 8 * l;
+    auto load = [&](int tt, int hh, uint4 (&w)[2]) {
+      const uint16_t* x = x0 + (long long)tt * s.xt + (long long)hh * s.xh;
+      if (tt < nt && l < chunks) w[0] = *reinterpret_cast<const uint4*>(x);
+      if (tt < nt && l + LP < chunks) w[1] = *reinterpret_cast<const uint4*>(x + 8 * LP);
+    };
+    uint4 w[2], wn[2];
+    w[0] = w[1] = wn[0] = wn[1] = make_uint4(0, 0, 0, 0);
+    load(t, h, w);
+    advance(tn, hn);
+    if (!filled) {
+      filled = true;
+      for (int i = threadIdx.x; i < nt * P; i += kThreadsR) {
+        const int tt = i / P, j = i - tt * P;
+        const int ax = p.pair_axis ? min((int)p.pair_axis[j], p.axes - 1) : 0;
+        const int pos = p.positions[(t0 + tt) * p.pos_stride + ax];
+        double angle = (double)pos * (double)p.inv_freq[j] * 0.15915494309189535;      // 1 / 2pi
+        angle -= rint(angle);
+        float sn, cn;
+        sincospif(2.0f * (float)angle, &sn, &cn);
+        table[inter ? 2 * i : i] = cn;
+        table[inter ? 2 * i + 1 : kMaxTable + i] = sn;
+      }
+      __syncthreads();
+    }
 
   // The loop bound is uniform over the CTA: every lane takes part in the
-  // shuffles, lanes of rows beyond the last with zeros.
+  // shuffles, lanes of rows beyond the last with what they hold.
   for (int r0 = 0; r0 < rows; r0 += kSlots) {
-    const int r = r0 + slot;
-    load(r + kSlots, wn);
-    const bool live = r < rows;
-    const int rr = live ? r : rows - 1;
-    const int tl = rr / nh;
-    int h = h0 + rr % nh;
-    const bool key = h >= p.q.heads;
-    const HeadSide& s = key ? p.k : p.q;
-    if (key) h -= p.q.heads;
-    float v[2][8];
-    unpack8<BF16>(w[0], v[0]);
-    unpack8<BF16>(w[1], v[1]);
+    load(tn, hn, wn);
+    const bool live = t < nt;
+    const int tl = live ? t : 0;
+    uint64_t v[2][4];
+    unpack4<BF16>(w[0], v[0]);
+    unpack4<BF16>(w[1], v[1]);
 
-    if (p.q.weight || p.k.weight) {                 // uniform: shuffles inside
-      float ss = 0.0f;
+    if (s.weight) {
+      uint64_t s2 = 0;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
+        for (int i = 0; i < 4; ++i) s2 = fma2(v[c][i], v[c][i], s2);
+      float ss = lo2(s2) + hi2(s2);
 #pragma unroll
       for (int o = 1; o < LP; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-      if (s.weight) {
-        const float rs = rsqrtf(ss / (float)D + p.eps);
+      const float rs = rsqrtf(fmaf(ss, inv_d, p.eps));
+      const uint64_t rs2 = pk2(rs, rs);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (l + LP * c < chunks) {
-            float g[8];
-            unpack8<BF16>(*(reinterpret_cast<const uint4*>(s.weight) + l + LP * c), g);
+      for (int c = 0; c < 2; ++c) {
+        const float* g = gain[side] + 8 * (l + LP * c);   // (16 LP of them: in range for lanes without a chunk too)
+        uint64_t g2[4];
+        load2(g, g2[0], g2[1]);
+        load2(g + 4, g2[2], g2[3]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * rs * g[i];
-          }
-        }
+        for (int i = 0; i < 4; ++i) v[c][i] = mul2(mul2(v[c][i], rs2), g2[i]);
       }
     }
 
     if (P > 0) {
-      const float2* tab = cs + tl * P;
-      if (p.interleaved) {
+      if (inter) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int p0 = 4 * (l + LP * c);
+          const float* e = table + 2 * (tl * P + p0);
+          if (whole || (p0 + 4 <= P && (P & 1) == 0)) {   // cos and sin of two pairs at once, 16-byte aligned
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (p0 + i < P) {
-              const float2 e = tab[p0 + i];
-              const float x0 = v[c][2 * i], x1 = v[c][2 * i + 1];
-              v[c][2 * i] = fmaf(x0, e.x, -(x1 * e.y));
-              v[c][2 * i + 1] = fmaf(x0, e.y, x1 * e.x);
+            for (int i = 0; i < 4; i += 2) {
+              const float4 cs = *reinterpret_cast<const float4*>(e + 2 * i);
+              turn(v[c][i], cs.x, cs.y);
+              turn(v[c][i + 1], cs.z, cs.w);
             }
+          } else if (p0 < P) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (p0 + i < P) turn(v[c][i], e[2 * i], e[2 * i + 1]);
           }
         }
       } else if (P == 8 * LP) {                      // the pair's halves are this lane's two chunks
+        const float* e = table + tl * P + 8 * l;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 e = tab[8 * l + i];
-          const float x0 = v[0][i], x1 = v[1][i];
-          v[0][i] = fmaf(x0, e.x, -(x1 * e.y));
-          v[1][i] = fmaf(x0, e.y, x1 * e.x);
+        for (int i = 0; i < 4; i += 2) {
+          uint64_t cn[2], sn[2];
+          load2(e + 2 * i, cn[0], cn[1]);
+          load2(e + kMaxTable + 2 * i, sn[0], sn[1]);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint64_t x0 = v[0][i + q], x1 = v[1][i + q];
+            v[0][i + q] = sub2(mul2(x0, cn[q]), mul2(x1, sn[q]));
+            v[1][i + q] = fma2(x0, sn[q], mul2(x1, cn[q]));
+          }
         }
       } else {                                       // P % 8 == 0: the other half is a whole chunk elsewhere
         const int pc = P / 8;
-        float o[2][8];
+        uint64_t o[2][4];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int ci = l + LP * c;
           const int other = ci < pc ? ci + pc : (ci < 2 * pc ? ci - pc : ci);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float u0 = __shfl_sync(0xFFFFFFFFu, v[0][i], other & (LP - 1), LP);
-            const float u1 = __shfl_sync(0xFFFFFFFFu, v[1][i], other & (LP - 1), LP);
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t u0 = __shfl_sync(0xFFFFFFFFu, v[0][i], other & (LP - 1), LP);
+            const uint64_t u1 = __shfl_sync(0xFFFFFFFFu, v[1][i], other & (LP - 1), LP);
             o[c][i] = other >= LP ? u1 : u0;
           }
         }
@@ -196,11 +239,17 @@ __global__ void __launch_bounds__(kThreadsR) qk_norm_rope_kernel(const __grid_co
           const int ci = l + LP * c;
           if (ci < 2 * pc) {
             const bool first = ci < pc;
-            const float2* e8 = tab + 8 * (first ? ci : ci - pc);
+            const float* e = table + tl * P + 8 * (first ? ci : ci - pc);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 e = e8[i];
-              v[c][i] = first ? fmaf(v[c][i], e.x, -(o[c][i] * e.y)) : fmaf(o[c][i], e.y, v[c][i] * e.x);
+            for (int i = 0; i < 4; i += 2) {
+              uint64_t cn[2], sn[2];
+              load2(e + 2 * i, cn[0], cn[1]);
+              load2(e + kMaxTable + 2 * i, sn[0], sn[1]);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint64_t x = v[c][i + q], y = o[c][i + q];
+                v[c][i + q] = first ? sub2(mul2(x, cn[q]), mul2(y, sn[q])) : fma2(y, sn[q], mul2(x, cn[q]));
+              }
             }
           }
         }
@@ -210,42 +259,55 @@ __global__ void __launch_bounds__(kThreadsR) qk_norm_rope_kernel(const __grid_co
     if (p.hadamard) {                                // D is a power of two; D = 8 has one chunk (LP = 1)
       const bool two = D >= 16;
 #pragma unroll
-      for (int hp = 1; hp < 8; hp <<= 1) {
+      for (int c = 0; c < 2; ++c) {
+        // Neighbours: two pairs give two sums and two differences.
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int i = 0; i < 4; i += 2) {
+          const uint64_t x = pk2(lo2(v[c][i]), lo2(v[c][i + 1])), y = pk2(hi2(v[c][i]), hi2(v[c][i + 1]));
+          const uint64_t sm = add2(x, y), df = sub2(x, y);
+          v[c][i] = pk2(lo2(sm), lo2(df));
+          v[c][i + 1] = pk2(hi2(sm), hi2(df));
+        }
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+        for (int hp = 1; hp < 4; hp <<= 1)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
             if ((i & hp) == 0) {
-              const float x0 = v[c][i], x1 = v[c][i + hp];
-              v[c][i] = x0 + x1;
-              v[c][i + hp] = x0 - x1;
+              const uint64_t x = v[c][i], y = v[c][i + hp];
+              v[c][i] = add2(x, y);
+              v[c][i + hp] = sub2(x, y);
             }
       }
 #pragma unroll
       for (int o = 1; o < LP; o <<= 1) {
         const float sg = (l & o) ? -1.0f : 1.0f;
+        const uint64_t sg2 = pk2(sg, sg);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[c][i] = fmaf(sg, v[c][i], __shfl_xor_sync(0xFFFFFFFFu, v[c][i], o));
+          for (int i = 0; i < 4; ++i) v[c][i] = fma2(sg2, v[c][i], __shfl_xor_sync(0xFFFFFFFFu, v[c][i], o));
       }
       const float scale = rsqrtf((float)D);
+      const uint64_t scale2 = pk2(scale, scale);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x0 = v[0][i], x1 = two ? v[1][i] : 0.0f;
-        v[0][i] = (x0 + x1) * scale;
-        v[1][i] = (x0 - x1) * scale;
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t x = v[0][i], y = two ? v[1][i] : 0;
+        v[0][i] = mul2(add2(x, y), scale2);
+        v[1][i] = mul2(sub2(x, y), scale2);
       }
     }
 
     if (live) {
-      uint16_t* y = static_cast<uint16_t*>(s.y) + (long long)(t0 + tl) * s.yt + h * s.yh;
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (l + LP * c < chunks) *reinterpret_cast<uint4*>(y + 8 * (l + LP * c)) = pack8<BF16>(v[c]);
+      uint16_t* y = y0 + (long long)t * s.yt + (long long)h * s.yh;
+      if (l < chunks) *reinterpret_cast<uint4*>(y) = pack4<BF16>(v[0]);
+      if (l + LP < chunks) *reinterpret_cast<uint4*>(y + 8 * LP) = pack4<BF16>(v[1]);
     }
     w[0] = wn[0];
     w[1] = wn[1];
+    t = tn;
+    h = hn;
+    advance(tn, hn);
+  }
   }
 }
 
@@ -256,19 +318,30 @@ cudaError_t launch(const QkNormRopeLaunch& p, cudaStream_t stream) {
   RowsArgs a;
   a.p = p;
   // Few tokens: one row per slot and the heads split over CTAs (latency).
-  // Otherwise a CTA takes all heads of enough tokens for four rows per slot,
-  // so that the loads of the next rows hide behind the current ones.
-  if ((long long)p.tokens * heads <= 4ll * 148 * kSlots) {
+  // Otherwise every resident CTA takes all heads of an equal share of the
+  // tokens, in as many rounds as the table of angles asks for.
+  const long long resident = (long long)kCtasR * p.num_sms;
+  if ((long long)p.tokens * heads <= resident * kSlots) {
     a.tb = heads >= kSlots ? 1 : kSlots / heads;
     a.hb = kSlots < heads ? kSlots : heads;
   } else {
-    a.tb = (4 * kSlots + heads - 1) / heads;
+    const int most = p.pairs > 0 ? kMaxTable / p.pairs : 1 << 20;
+    const long long share = (p.tokens + resident - 1) / resident, rounds = (share + most - 1) / most;
+    a.tb = (int)((p.tokens + resident * rounds - 1) / (resident * rounds));
     a.hb = heads;
   }
-  if (p.pairs > 0 && a.tb * p.pairs > kMaxTable) a.tb = kMaxTable / p.pairs;    // pairs <= 128
+  if (p.pairs > 0 && a.tb > kMaxTable / p.pairs) a.tb = kMaxTable / p.pairs;    // pairs <= 128
   const dim3 grid((unsigned)((p.tokens + a.tb - 1) / a.tb), (unsigned)((heads + a.hb - 1) / a.hb));
-  qk_norm_rope_kernel<BF16, LOGLP><<<grid, kThreadsR, 0, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreadsR);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<BF16, LOGLP>, a);
 }
 
 template <bool BF16>
