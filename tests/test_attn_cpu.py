@@ -47,12 +47,6 @@ def test_structures_match_the_header(tmp_path):
     for n in names:
         want += [getattr(getattr(S, n), f).offset for f, *_ in getattr(S, n)._fields_]
     assert got == want
-    from bit_quantized_linear_svdq_b200 import attention as A
-    for packed, n in ((A._HEADS, "svdq_heads"), (A._ROPE, "svdq_qk_norm_rope_desc"), (A._CACHE, "svdq_kv4_cache"),
-                      (A._ATTENTION, "svdq_kv4_attention_desc")):
-        assert packed.size == ctypes.sizeof(getattr(S, n))
-    fields = iter(range(1, 100))
-    assert bytes(S.svdq_kv4_cache(*[next(fields) for _ in range(8)])) == A._CACHE.pack(*range(1, 9))
 
 
 def test_rows_and_keys_of_the_tiles(tmp_path):
@@ -177,6 +171,14 @@ def test_wrappers_refuse_cpu_tensors():
         S.kv4_attention(q, cache, torch.zeros(2, dtype=torch.int32), torch.zeros(2, 1, dtype=torch.int32))
     with pytest.raises(TypeError):
         S.qk_norm_rope([1.0])
+
+
+def test_missing_extension_module_fails_loudly(lib, monkeypatch, tmp_path):
+    from bit_quantized_linear_svdq_b200 import attention as A
+    monkeypatch.setattr(A, "_native", None)
+    monkeypatch.setattr(S, "library_path", lambda: str(tmp_path / "libsvdq_b200.so"))
+    with pytest.raises(RuntimeError, match="not built"):
+        A._calls()
 
 
 @pytest.mark.parametrize("args", [(0, 16, 2, 128), (2, 24, 2, 128), (2, 16, 0, 128), (2, 16, 2, 96)])
