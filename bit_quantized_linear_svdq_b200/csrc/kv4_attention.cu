@@ -50,9 +50,10 @@ namespace svdq {
 namespace {
 
 constexpr int kWarpsA = 4, kThreadsA = 32 * kWarpsA, kTileA = 32, kStagesA = 2;
-// Resident CTAs an SM by rows of a tile / 8: what the accumulators leave room for.
-__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
-
+// Resident CTAs an SM by head dimension and rows of a tile / 8: what the accumulators leave room for.
+__host__ __device__ constexpr int ctas_per_sm(int d, int nt) {
+  return d == 64 ? (nt == 1 ? 5 : nt == 2 ? 4 : nt == 3 ? 3 : 2) : (nt == 1 ? 4 : nt == 2 ? 3 : 2);
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -81,7 +82,7 @@ template <int D, int NT>
 constexpr int smem_bytes() {
   const int ring = kWarpsA * kStagesA * Tile<D>::kStage;
   const int join = kWarpsA * 8 * NT * (D + 4) * 4 + kWarpsA * 8 * NT * 8;
-  return (ring > join ? ring : join) + NT * (D / 32) * 512 + 8 * NT * 4;
+  return (ring > join ? ring : join) + NT * (D / 32) * 512 + 8 * NT * 8;
 }
 
 // Keys [k_begin, k_end) of one segment: its rows' unnormalized outputs, maxima
@@ -152,29 +153,34 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
     }
     cp_commit();
   };
+  // The queries' loads first: they are under way while the page numbers come.  Lane (g, t) takes row g of an 8-row tile, a
+  // quarter of the head; warp w the tile w (NT <= 4).
+  static_assert(NT <= kWarpsA, "one 8-row tile a warp");
+  uint4 q_raw[D / 32];
+  int q_sees = 0;                                         // keys that this row sees
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) q_raw[i] = make_uint4(0, 0, 0, 0);
+  if (warp < NT && 8 * warp + g < rt.rows) {
+    const int row = rt.row0 + 8 * warp + g, tok = (int)((uint32_t)row / (uint32_t)group);
+    const int head = kvh * group + row - tok * group;
+    q_sees = rt.keys_of(tok, p.causal);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                      (long long)(rt.token0 + tok) * p.qt + head * p.qh + t * (D / 4));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) q_raw[i] = src[i];
+  }
 #pragma unroll
   for (int s = 0; s < kStagesA - 1; ++s) issue(s);
 
-  // ---- queries, as the first product's column operand: in shared memory, for every two MMA steps one 16-byte piece a
-  // lane.  Lane (g, t) prepares row g of an 8-row tile, a quarter of the head; warp w the tiles w, w + 4, ...
-  constexpr int kQ = smem_bytes<D, NT>() - NT * (D / 32) * 512 - kRows * 4;
+  // ---- queries, as the first product's column operand: in shared memory, for every two MMA steps one 16-byte piece a lane
+  constexpr int kQ = smem_bytes<D, NT>() - NT * (D / 32) * 512 - kRows * 8;
   uint4* qsm = reinterpret_cast<uint4*>(smem + kQ);                             // [NT][D / 32][32 lanes]
   float* back = reinterpret_cast<float*>(smem + kQ + NT * (D / 32) * 512);      // [rows] scale * log2e / 2^shift
-  auto keys_of_row = [&](int r) {
-    return r < rt.rows ? rt.keys_of((rt.row0 + r) / group, p.causal) : 0;
-  };
-  for (int n = warp; n < NT; n += kWarpsA) {
-    const int r = 8 * n + g;
+  int* sees = reinterpret_cast<int*>(back + kRows);                             // [rows] keys that the row sees
+  if (warp < NT) {
     float f[D / 4];
 #pragma unroll
-    for (int i = 0; i < D / 4; ++i) f[i] = 0.0f;
-    if (r < rt.rows) {
-      const int row = rt.row0 + r, tok = row / group, head = kvh * group + row - tok * group;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                        (long long)(rt.token0 + tok) * p.qt + head * p.qh + t * (D / 4));
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) unpack8<BF16>(src[i], f + 8 * i);
-    }
+    for (int i = 0; i < D / 32; ++i) unpack8<BF16>(q_raw[i], f + 8 * i);
     // Power of two that takes the row's largest finite magnitude to [2^14, 2^15).
     float big = 0.0f;
 #pragma unroll
@@ -183,10 +189,13 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
     big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
     const int e = row_exponent(big);
     const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-    if (t == 0) back[r] = p.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
+    if (t == 0) {
+      back[8 * warp + g] = p.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
+      sees[8 * warp + g] = q_sees;
+    }
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
-      qsm[(n * (D / 32) + i) * 32 + lane] =
+      qsm[(warp * (D / 32) + i) * 32 + lane] =
           make_uint4(half2u(f[8 * i] * up, f[8 * i + 1] * up), half2u(f[8 * i + 2] * up, f[8 * i + 3] * up),
                      half2u(f[8 * i + 4] * up, f[8 * i + 5] * up), half2u(f[8 * i + 6] * up, f[8 * i + 7] * up));
   }
@@ -198,10 +207,10 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       qs[n][c] = back[8 * n + 2 * t + c];
-      lim[n][c] = keys_of_row(8 * n + 2 * t + c);
+      lim[n][c] = sees[8 * n + 2 * t + c];
     }
   // Tiles that end at or before the first row's keys need no mask.
-  const int free_end = min(rt.keys_of(rt.row0 / group, p.causal), k_end);
+  const int free_end = min(rt.keys_of((int)((uint32_t)rt.row0 / (uint32_t)group), p.causal), k_end);
 
   // Rows 2t, 2t + 1 of each tile: reference exponent (base 2), sum of weights, outputs.
   float o[NT][kDM][4], ref[NT][2], sum[NT][2];
@@ -370,7 +379,7 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
           const int kt = k0 + 16 * u + t;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const int see = keys_of_row(8 * n + g);
+            const int see = sees[8 * n + g];
             uint32_t b[2];
             float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -458,7 +467,7 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
       v[0] = fmaf(a.x, f, v[0]), v[1] = fmaf(a.y, f, v[1]), v[2] = fmaf(a.z, f, v[2]), v[3] = fmaf(a.w, f, v[3]);
       v[4] = fmaf(b.x, f, v[4]), v[5] = fmaf(b.y, f, v[5]), v[6] = fmaf(b.z, f, v[6]), v[7] = fmaf(b.w, f, v[7]);
     }
-    const int row = rt.row0 + r, tok = row / group, head = kvh * group + row - tok * group;
+    const int row = rt.row0 + r, tok = (int)((uint32_t)row / (uint32_t)group), head = kvh * group + row - tok * group;
     const long long token = rt.token0 + tok;
     if (whole) {
       store_row8<BF16>(p, token, head, d0, v, top, total);
@@ -473,13 +482,13 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
 }
 
 template <int D, int NT, bool BF16>
-__global__ void __launch_bounds__(kThreadsA, ctas_per_sm(NT))
+__global__ void __launch_bounds__(kThreadsA, ctas_per_sm(D, NT))
     kv4_attention_kernel(const __grid_constant__ Kv4AttnLaunch p) {
   griddep_wait();
   griddep_launch_dependents();
   const Kv4Work w = work_of(p);
   const WarpUnits wu = warp_units(w);
-  const long long per = (wu.total + gridDim.x - 1) / gridDim.x;
+  const long long per = kv4_div(wu.total + gridDim.x - 1, gridDim.x);
   const long long u0 = per * blockIdx.x, u1 = min(u0 + per, wu.total);
   bool noted = false;
   for (long long u = u0; u < u1;) {
@@ -492,7 +501,7 @@ __global__ void __launch_bounds__(kThreadsA, ctas_per_sm(NT))
                                 min(sg.tile.last_key, (sg.unit0 + n) * kUnitKeys), whole,
                                 2ll * blockIdx.x + (u == u0 ? 0 : 1));
     if (!whole && sg.unit0 == 0) {
-      if (threadIdx.x == 0) p.cuts[blockIdx.x] = cut_of(sg.tile, sg.head, (int)((u + sg.units - 1) / per), u == u0 ? 0 : 1);
+      if (threadIdx.x == 0) p.cuts[blockIdx.x] = cut_of(sg.tile, sg.head, (int)kv4_div(u + sg.units - 1, per), u == u0 ? 0 : 1);
       noted = true;
     }
     u += n;
@@ -634,6 +643,7 @@ template <int D, bool BF16>
 cudaError_t launch_few(const Kv4AttnLaunch& p, cudaStream_t stream) {
   if (p.tile_rows == 8) return launch_nt<D, 1, BF16>(p, stream);
   if (p.tile_rows == 16) return launch_nt<D, 2, BF16>(p, stream);
+  if (p.tile_rows == 24) return launch_nt<D, 3, BF16>(p, stream);
   return launch_nt<D, 4, BF16>(p, stream);
 }
 template <int D, bool BF16>
@@ -699,9 +709,12 @@ Kv4Plan kv4_attention_plan(const Kv4AttnLaunch& base, int max_kv, int num_sms) {
   // The smallest tile that holds an average request's rows: a larger one
   // dequantizes each key for more rows at once, a smaller one leaves room for
   // more warps.
-  const long long share = plan.use_many && plan.use_few ? kFewRows : rows;
-  const int nt = share <= 8ll * base.requests ? 1 : share <= 16ll * base.requests ? 2 : 4;
-  plan_launch(plan.few, 8 * nt, 0, plan.use_many ? kFewRows : kAll, (long long)num_sms * ctas_per_sm(nt), max_kv);
+  // Unequal requests (q_start): half as much again, so that most still fit one
+  // tile; beside prompts, single tokens.
+  long long each = base.requests > 0 ? (rows + base.requests - 1) / base.requests : 0;
+  if (base.q_start) each = plan.use_many ? base.q_heads / base.c.heads : each + each / 2;
+  const int nt = each <= 8 ? 1 : each <= 16 ? 2 : each <= 24 ? 3 : 4;
+  plan_launch(plan.few, 8 * nt, 0, plan.use_many ? kFewRows : kAll, (long long)num_sms * ctas_per_sm(base.c.D, nt), max_kv);
   plan_launch(plan.many, 256, plan.use_few ? kFewRows + 1 : 0, kAll, num_sms, max_kv);
   return plan;
 }

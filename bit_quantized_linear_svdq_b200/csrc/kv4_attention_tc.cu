@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
   griddep_launch_dependents();
   const Kv4Work w = work_of(p);
   const WarpUnits wu = warp_units(w);
-  const long long per = (wu.total + gridDim.x - 1) / gridDim.x;
+  const long long per = kv4_div(wu.total + gridDim.x - 1, gridDim.x);
   const long long u0 = per * blockIdx.x, u1 = min(u0 + per, wu.total);
   const int group = p.q_heads / p.c.heads;
 
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
     for (long long u = u0; ok && u < u1;) {
       const Job job = next_job(w, wu, u, u0, u1);
       if (!job.whole && job.begun) {
-        if (key == 0) p.cuts[blockIdx.x] = cut_of(job.rt, job.head, (int)((u + job.units - 1) / per), job.slot);
+        if (key == 0) p.cuts[blockIdx.x] = cut_of(job.rt, job.head, (int)kv4_div(u + job.units - 1, per), job.slot);
         noted = true;
       }
       u += job.tiles;

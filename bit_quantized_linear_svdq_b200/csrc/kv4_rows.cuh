@@ -21,6 +21,12 @@ namespace svdq {
 
 KV4_HD int kv4_min(long long a, long long b) { return (int)(a < b ? a : b); }
 KV4_HD int kv4_max(long long a, long long b) { return (int)(a > b ? a : b); }
+// a / b for a >= 0, b > 0, by 32-bit division where both fit (a 64-bit one
+// costs about 500 cycles; five of them in a row were most of the set-up).
+KV4_HD long long kv4_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
 
 struct RequestSpan {
   int token0, n, keys;                          // first token, tokens, keys
@@ -57,10 +63,12 @@ KV4_HD RowTile tile_of(const RequestSpan& s, int b, int group, int tile_rows, lo
   r.token0 = s.token0;
   r.n = s.n;
   r.keys = s.keys;
-  const long long row0 = tile * tile_rows, all = (long long)s.n * group;
-  r.row0 = (int)row0;
-  r.rows = row0 < all ? kv4_min(tile_rows, all - row0) : 0;
-  r.last_key = r.rows > 0 ? keys_seen(s.keys, s.n, (int)((row0 + r.rows - 1) / group), causal) : 0;
+  // (tokens x query heads fits 31 bits: checked at the call)
+  const int row0 = (int)tile * tile_rows, all = s.n * group;
+  r.row0 = row0;
+  r.rows = row0 < all ? (all - row0 < tile_rows ? all - row0 : tile_rows) : 0;
+  const int last = r.rows > 0 ? (int)((uint32_t)(row0 + r.rows - 1) / (uint32_t)group) : 0;
+  r.last_key = r.rows > 0 ? keys_seen(s.keys, s.n, last, causal) : 0;
   return r;
 }
 
@@ -81,13 +89,14 @@ struct Kv4Work {
 };
 KV4_HD RequestSpan span_of(const Kv4Work& w, int b) {
   RequestSpan s = request_span(w.q_start, w.kv_len, w.requests, w.tokens, b, w.capacity);
-  const long long rows = (long long)s.n * w.group;
+  const int rows = s.n * w.group;
   if (rows < w.min_rows || rows > w.max_rows) s.n = 0;
   return s;
 }
-KV4_HD int tile_units(int last_key) { return last_key > 0 ? (last_key - 1) / kUnitKeys + 1 : 1; }
+KV4_HD int tile_units(int last_key) { return last_key > 0 ? (int)((uint32_t)(last_key - 1) / kUnitKeys) + 1 : 1; }
 KV4_HD int tiles_of(const Kv4Work& w, const RequestSpan& s) {
-  return (int)(((long long)s.n * w.group + w.tile_rows - 1) / w.tile_rows);
+  const int rows = s.n * w.group;
+  return rows <= w.tile_rows ? (rows > 0 ? 1 : 0) : (int)((uint32_t)(rows + w.tile_rows - 1) / (uint32_t)w.tile_rows);
 }
 // Steps through a request's tiles: the token of each tile's last row, without
 // a division a tile.
@@ -113,7 +122,8 @@ struct TileWalk {
 // Units of a request under one head.
 KV4_HD long long head_units(const Kv4Work& w, const RequestSpan& s) {
   const int nt = tiles_of(w, s);
-  if (!w.causal) return (long long)nt * tile_units(s.keys);
+  // One tile, or tiles that all see the same keys: its last row is the request's last token, which sees every key.
+  if (!w.causal || nt <= 1) return (long long)nt * tile_units(s.keys);
   TileWalk walk(w, s);
   long long u = 0;
   for (int t = 0; t < nt; ++t, walk.next()) u += tile_units(keys_seen(s.keys, s.n, walk.last_token(), 1));
@@ -127,12 +137,12 @@ struct Segment {
 KV4_HD Segment segment_in(const Kv4Work& w, const RequestSpan& s, int b, long long u) {
   const long long per_head = head_units(w, s);
   Segment g;
-  g.head = (int)(u / per_head);
+  g.head = (int)kv4_div(u, per_head);
   u -= g.head * per_head;
   int t = 0;
-  if (!w.causal) {
+  if (!w.causal || s.n * w.group <= w.tile_rows) {
     g.units = tile_units(s.keys);
-    t = (int)(u / g.units);
+    t = u < g.units ? 0 : (int)kv4_div(u, g.units);
     u -= (long long)t * g.units;
   } else {
     TileWalk walk(w, s);
