@@ -6,15 +6,19 @@
 // value is dequantized once for 256 rows.  At that many rows the products
 // bound it (4 D flops a row and key: D = 128, 2048 cycles a tile), and next to
 // them the exponentials (one a row and key: as many cycles of the special
-// function unit).  Measured about 4500 cycles a tile, 0.7 PFLOP/s: a half's
-// chain from scores to weights (about 3000) and back through its two products
-// is not hidden altogether by the other half's.
+// function unit).  Measured about 3900 cycles a tile, 0.82 PFLOP/s on chunks of
+// up to 1024 tokens behind 8203 keys and 0.92 on 4096 queries of 32 heads over
+// 4333 keys (0.5 and 0.56 of the measured bf16 rate): a half's chain from scores
+// to weights and back through its two products is not hidden altogether by the
+// other half's.
 //
-// Roles (one CTA per SM; 152, 152, 112 and 96 registers a thread):
+// Roles (one CTA per SM; 176, 176, 88 and 72 registers a thread):
 //   warps 0-3, 4-7   softmax of half 0 and 1: thread = row = tensor memory lane.
-//                    Scores come from tensor memory, weights go back there as
-//                    fp16 over the scores; the output is rescaled there only
-//                    when the reference exponent rises by more than 8.
+//                    A row's 128 scores come from tensor memory into registers
+//                    (with 152 registers and half of them read twice: 266 us
+//                    against 231), weights go back there as fp16 over the
+//                    scores; the output is rescaled there only when the
+//                    reference exponent rises by more than 8.
 //   warps 8-11       thread = key of the tile: 4-bit rows -> fp16 rows in shared
 //                    memory, K and V in the same layout (128-byte swizzled rows
 //                    of 64 dims): K is the first product's K-major operand, V
@@ -24,10 +28,11 @@
 //                    turn, so that one half's softmax runs beside the other's
 //                    products; each half's outputs begin with the first 64
 //                    weights a row.
-// Measured and left out (prompt of 2 x 1024 tokens behind 8203 keys, 275 us):
-// 64-key sub-tiles with scores double-buffered (N = 64 MMAs take 48 cycles, not
-// 32: 302 us); two threads a row on 16 warps (284 us); a quarter to a half of
-// the exponentials as polynomials on the FMA pipe (298 to 347 us).
+// Measured and left out (the prompt chunks above, 231 us): 64-key sub-tiles with
+// scores double-buffered (an MMA of N = 64 takes 48 cycles, not 32: 302 us
+// against 284 at the time); two threads a row on 16 warps (284 against 275); an
+// eighth to a half of the exponentials as polynomials on the FMA pipe (235 to 280
+// us); the halves' exponentials taking turns (287 against 266).
 // Tensor memory: S_h (128 columns, P over the last 64), O_0 O_1 (D each).
 // Shared memory: Q 2 x 128 x D, two stages of K and of V (128 x D each), fp16.
 //
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax of half h, row = lane of tensor memory
-    set_registers<true, 152>();
+    set_registers<true, 176>();
     const int h = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;     // lane field (bits 31:16) of this warp's quadrant
     const uint32_t s_tm = tmem + lanes + h * kKeys, o_tm = tmem + lanes + 2 * kKeys + h * D;
@@ -340,26 +345,21 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
         const uint32_t absent = (uint32_t)misc[2 + (n_all & 3)];
         const bool masked = partial || absent != 0;
         const int see = lim - k0;                         // columns below it are visible
-        // ---- maximum of the visible scores; the last 64 columns stay in registers
-        uint32_t v0[32], v1[32];
+        // ---- the row's scores, and the maximum of the visible ones
+        uint32_t v[4][32];
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          tmem_ld32(s_tm + 64 * x, v0);
-          tmem_ld32(s_tm + 64 * x + 32, v1);
-          tmem_ld_wait();
-          if (masked) {
-            mask32(v0, see - 64 * x, absent >> (16 * x));
-            mask32(v1, see - 64 * x - 32, absent >> (16 * x + 8));
-          }
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, v[c]);
+        tmem_ld_wait();
+        if (masked) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            tops[0] = max3(tops[0], __uint_as_float(v0[i]), __uint_as_float(v0[i + 1]));
-            tops[1] = max3(tops[1], __uint_as_float(v0[i + 2]), __uint_as_float(v0[i + 3]));
-            tops[2] = max3(tops[2], __uint_as_float(v1[i]), __uint_as_float(v1[i + 1]));
-            tops[3] = max3(tops[3], __uint_as_float(v1[i + 2]), __uint_as_float(v1[i + 3]));
-          }
+          for (int c = 0; c < 4; ++c) mask32(v[c], see - 32 * c, absent >> (8 * c));
         }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            tops[c] = max3(tops[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
         const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
         // Relative to the reference (the first key's own, then raised past 2^8 only).
         const float rel = ref == -INFINITY ? top * qs : fmaf(top, qs, -ref);
@@ -397,19 +397,13 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
           }
           tmem_st16(to, pw);
         };
-        weights(v0, s_tm + 96);
-        tmem_ld32(s_tm, v0);
-        weights(v1, s_tm + 112);
-        tmem_ld_wait();
-        tmem_ld32(s_tm + 32, v1);
+        weights(v[2], s_tm + 96);
+        weights(v[3], s_tm + 112);
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(ctl.bar(kPFull + 2 * h + 1));
-        if (masked) mask32(v0, see, absent);
-        weights(v0, s_tm + 64);
-        tmem_ld_wait();
-        if (masked) mask32(v1, see - 32, absent >> 8);
-        weights(v1, s_tm + 80);
+        weights(v[0], s_tm + 64);
+        weights(v[1], s_tm + 80);
         const uint64_t both = add2(part[0], part[1]);
         sum += lo2(both) + hi2(both);
         if (partial) {                                    // rows see it in part: NaN values were taken out
@@ -487,7 +481,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ dequantize: thread = key of the tile
-    set_registers<false, 112>();
+    set_registers<false, 88>();
     const int key = threadIdx.x - 256;
     long long n_all = 0;
     bool ok = true;
@@ -543,7 +537,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
     }
     if (p.join && !noted && key == 0) p.cuts[blockIdx.x].rows = 0;
   } else {
-    set_registers<false, 96>();
+    set_registers<false, 72>();
     if (warp == 12) {
     // ------------------------------------------------------------ MMA
     constexpr uint32_t kIdS = idesc_f16(kHalf, kKeys, false), kIdO = idesc_f16(kHalf, D, true);
