@@ -304,33 +304,42 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
       const int head = job.head * group + abs_row - tok * group;
       const int lim = live ? job.rt.keys_of(tok, p.causal) : 0;
       const int free_end = min(job.rt.keys_of(job.rt.row0 / group, p.causal), job.k_end);
-      // ---- queries: scaled by a power of two to [2^14, 2^15) at the row's largest finite magnitude
-      float qs;
+      // ---- queries: scaled by a power of two to [2^14, 2^15) at the row's largest finite magnitude.  A warp loads whole
+      // rows of its 32 (D / 8 lanes a row: a load of one row a lane touches 32 lines at once), each lane learns its
+      // row's address from the row's owner and leaves it the factor.
+      constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;      // 16-byte pieces of a row, rows a load
+      const int mine = lane % kPieces, which = lane / kPieces;
+      const uint32_t tile = base + SM::kQ + h * SM::kTile;
+      float qs = 0.0f;
       {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                          (long long)(job.rt.token0 + tok) * p.qt + head * p.qh);
-        uint4 packed[D / 8];
+        const long long at = (long long)(job.rt.token0 + tok) * p.qt + (long long)head * p.qh;
+        uint4 packed[kPieces];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) packed[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
-        float big = 0.0f;
+        for (int i = 0; i < kPieces; ++i) {
+          const int rr = kAtOnce * i + which;
+          const long long from = __shfl_sync(0xFFFFFFFFu, at, rr);
+          const bool there = h * kHalf + 32 * (warp & 3) + rr < job.rt.rows;
+          packed[i] = there ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + from + 8 * mine)
+                            : make_uint4(0, 0, 0, 0);
+        }
+        const float sign = p.scale < 0.0f ? -1.0f : 1.0f;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          float f[8];
+        for (int i = 0; i < kPieces; ++i) {
+          const int rr = kAtOnce * i + which;
+          float f[8], big = 0.0f;
           unpack8<BF16>(packed[i], f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(f[j]) < INFINITY ? fabsf(f[j]) : 0.0f);
-        }
-        const int e = row_exponent(big);
-        const float sign = p.scale < 0.0f ? -1.0f : 1.0f;
-        const float up = sign * __uint_as_float((uint32_t)(127 + e) << 23);
-        qs = sign * p.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
-        const uint32_t q_tile = base + SM::kQ + h * SM::kTile;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          float f[8];
-          unpack8<BF16>(packed[i], f);
-          st_shared_v4(q_tile + tile_offset(r, i), make_uint4(half2u(f[0] * up, f[1] * up), half2u(f[2] * up, f[3] * up),
-                                                              half2u(f[4] * up, f[5] * up), half2u(f[6] * up, f[7] * up)));
+          for (int o = 1; o < kPieces; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+          const int e = row_exponent(big);
+          const float up = sign * __uint_as_float((uint32_t)(127 + e) << 23);
+          st_shared_v4(tile + tile_offset(32 * (warp & 3) + rr, mine),
+                       make_uint4(half2u(f[0] * up, f[1] * up), half2u(f[2] * up, f[3] * up), half2u(f[4] * up, f[5] * up),
+                                  half2u(f[6] * up, f[7] * up)));
+          const float down = sign * p.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
+          const float theirs = __shfl_sync(0xFFFFFFFFu, down, (lane % kAtOnce) * kPieces);
+          if (lane / kAtOnce == i) qs = theirs;             // row kAtOnce * i + lane % kAtOnce is this lane's
         }
         fence_proxy_async_smem();
         mbar_arrive(ctl.bar(kQFull + h));
@@ -417,55 +426,57 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
         mbar_arrive(ctl.bar(kPFull + 2 * h));
       }
       if (!ok) break;
-      // ---- output: through this half's query tile (its scores are all done), so that rows are written whole
+      // ---- output: through the rows' own places in the query tile (the half's scores are all done), so that a warp
+      // writes whole rows of its 32
       if (!(ok = ctl.wait_warp(kOFull + h, n_job))) break;
       ++n_job;
       tc_fence_after_sync();
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       const long long part_row = (2ll * blockIdx.x + job.slot) * p.tile_rows;
-      const uint32_t tile = base + SM::kQ + h * SM::kTile;
-      constexpr int kPieces = D / 8;                      // 16-byte pieces of a row: D 16-bit or D / 2 fp32 values
+      const long long to = job.whole ? (long long)(job.rt.token0 + tok) * p.ot + (long long)head * p.oh : (part_row + row) * D;
+      // A pass: D 16-bit or D / 2 fp32 values a row.
       for (int pass = 0; pass < (job.whole ? 1 : 2); ++pass) {
 #pragma unroll 1
-        for (int c = 0; c < (job.whole ? D / 16 : D / 32); ++c) {
-          uint32_t y[16];
-          const int c16 = pass * (D / 32) + c;            // 16 columns, one block of the cache's format
-          tmem_ld16(o_tm + 16 * c16, y);
+        for (int c = 0; c < (job.whole ? D / 32 : D / 64); ++c) {
+          uint32_t y[32];
+          const int c32 = pass * (D / 64) + c;            // 32 columns, two blocks of the cache's format
+          tmem_ld32(o_tm + 32 * c32, y);
           tmem_ld_wait();
-          if ((poison >> c16) & 1u) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = 0x7FC00000u;
-          }
+          for (int b = 0; b < 2; ++b)
+            if ((poison >> (2 * c32 + b)) & 1u) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) y[16 * b + i] = 0x7FC00000u;
+            }
           if (job.whole) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) {
               uint32_t o[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const float a = __uint_as_float(y[8 * i + 2 * k]) * inv, b = __uint_as_float(y[8 * i + 2 * k + 1]) * inv;
                 o[k] = BF16 ? pack_bf16x2(a, b) : half2u(a, b);
               }
-              st_shared_v4(tile + r * 16 * kPieces + (((2 * c + i) ^ (r & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+              st_shared_v4(tile + tile_offset(r, 4 * c + i), make_uint4(o[0], o[1], o[2], o[3]));
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              st_shared_v4(tile + r * 16 * kPieces + (((4 * c + i) ^ (r & 7)) << 4),
+            for (int i = 0; i < 8; ++i)
+              st_shared_v4(tile + tile_offset(r, 8 * c + i),
                            make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]));
           }
         }
         __syncwarp();
-        const int first = 32 * (warp & 3);                // this warp's rows of the half
-        for (int i = lane; i < 32 * kPieces; i += 32) {
-          const int rr = first + i / kPieces, c = i % kPieces, in_tile = h * kHalf + rr;
-          if (in_tile >= job.rt.rows) break;              // (rows ascend)
-          const uint4 y = ld_shared_v4(tile + rr * 16 * kPieces + ((c ^ (rr & 7)) << 4));
-          if (job.whole) {
-            const int a = job.rt.row0 + in_tile, tk = a / group;
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (long long)(job.rt.token0 + tk) * p.ot +
-                                      (job.head * group + a - tk * group) * p.oh + 8 * c) = y;
-          } else {
-            *reinterpret_cast<uint4*>(p.part_o + (part_row + in_tile) * D + pass * (D / 2) + 4 * c) = y;
+#pragma unroll 4
+        for (int i = 0; i < kPieces; ++i) {
+          const int rr = kAtOnce * i + which;
+          const long long dst = __shfl_sync(0xFFFFFFFFu, to, rr);
+          if (h * kHalf + 32 * (warp & 3) + rr < job.rt.rows) {
+            const uint4 y = ld_shared_v4(tile + tile_offset(32 * (warp & 3) + rr, mine));
+            if (job.whole)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + dst + 8 * mine) = y;
+            else
+              *reinterpret_cast<uint4*>(p.part_o + dst + pass * (D / 2) + 4 * mine) = y;
           }
         }
         __syncwarp();

@@ -325,7 +325,7 @@ cudaError_t launch(const QkNormRopeLaunch& p, cudaStream_t stream) {
     a.tb = heads >= kSlots ? 1 : kSlots / heads;
     a.hb = kSlots < heads ? kSlots : heads;
   } else {
-    const int most = p.pairs > 0 ? kMaxTable / p.pairs : 1 << 20;
+    const int most = p.pairs > 0 ? kMaxTable / p.pairs : kMaxTable;
     const long long share = (p.tokens + resident - 1) / resident, rounds = (share + most - 1) / most;
     a.tb = (int)((p.tokens + resident * rounds - 1) / (resident * rounds));
     a.hb = heads;

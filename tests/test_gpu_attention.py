@@ -405,6 +405,31 @@ def test_attention(case):
     assert S.svdq_kv4_attention_status() == 0
 
 
+@pytest.mark.parametrize("d,keys", [(64, 50), (128, 50), (128, 300)])
+def test_many_row_tiles_a_block(d, keys):
+    """More (row tile, head) pairs than resident blocks, each over few keys: blocks go from one to the next, whole and
+    cut ones.  Without an order all queries see all keys, so the reference is one softmax."""
+    tokens, h = 6000, 16
+    g = gen(d + keys)
+    cache = filled_cache(g, -(-keys // 16) + 1, 16, h, d)
+    table = tables(g, [keys], 16, cache[0].shape[0])
+    q = heads(g, tokens, h, d, BF)
+    lens = torch.tensor([keys], dtype=torch.int32, device="cuda")
+    j = torch.arange(keys, device="cuda")
+    kb, vb = (values(cache, i)[table[0, j // 16].long(), j % 16].transpose(0, 1) for i in (0, 2))     # (heads, keys, dim)
+    sc = q.double().transpose(0, 1) @ kb.transpose(1, 2) / math.sqrt(d)
+    p, want_lse = torch.softmax(sc, -1), torch.logsumexp(sc, -1).t()
+    # (The bounds of attend_reference, with the largest score's for all.)
+    ds = 2.0 ** -23 * (d + 4) * float((q.double().abs().transpose(0, 1) @ kb.abs().transpose(1, 2)).max()) / math.sqrt(d) \
+        + 2.0 ** -22 * (float(sc.abs().max()) + 1)
+    want = (p @ vb).transpose(0, 1)
+    bound = (2.0 ** -11 + 2 * ds + 2 * keys * 2.0 ** -24) * (p @ vb.abs()).transpose(0, 1) + 2.0 ** -25 * vb.abs().sum(1)
+    for _ in range(5):
+        out, lse = S.kv4_attention(q, cache, lens, table, causal=False, return_lse=True)
+        assert_rounded(out, want, bound, BF)
+        assert ((lse.double() - want_lse).abs() <= ds + keys * 2.0 ** -24 + 2.0 ** -22 * (1 + want_lse.abs())).all()
+
+
 def test_attention_strided_arguments():
     g = gen(21)
     case = ([90, 31], [0, 2, 5], 4, 2, 128, 16, True, BF)
