@@ -8,7 +8,7 @@
 // a query that sees no key gets o = 0 and lse = -inf.
 //
 // Work split.  The query heads that share a key head, times the request's
-// tokens, are the rows of one tile (16 or 32).  One resident set of CTAs takes
+// tokens, are the rows of one tile (8, 16, 24 or 32).  One resident set of CTAs takes
 // equal shares of all keys of all tiles and heads (kv4_rows.cuh), so unequal
 // lengths and counts that do not divide leave no SM idle; a share starts and
 // ends wherever it falls.  A CTA's four warps alternate 32-key tiles and join
@@ -34,9 +34,15 @@
 // so that one convert gives the pair of keys an MMA operand wants.  Only the
 // weights change lanes (an 8x8 transpose, movmatrix).
 //
-// Bound: codes and scales are 9/16 byte a value, read once (HBM) with a ring of
-// cp.async copies per warp (no barrier between warps); dequantizing costs
-// about 1.2 instructions a value and lane, the same order as the memory time.
+// Bound: codes and scales are 9/16 byte a value, read once (HBM), through a ring
+// of cp.async copies per warp (no barrier between warps).  Above that lies the
+// instruction issue: about 620 warp instructions per 32 keys of one head (D =
+// 128, up to 8 rows) at 3.2 a clock, of which 256 convert and scale the 8192
+// values (cvt.e2m1x2 takes any byte of a register; the same from shifts and
+// logic is 2.2 times slower).  64 sequences of up to 8192 keys, 32 query and 8
+// key heads: 103 us, 4.4 TB/s; two of 131059 keys, 4 key heads: 40 us, 3.7 TB/s;
+// one of 1021 keys: 8.0 us, set-up and latencies.  16-key tiles: 128 us on the
+// first; five CTAs an SM, with spills, 129.
 //
 // Keys past L, pages outside the cache and everything masked for a row
 // contribute nothing, NaN included: such rows of the ring are zero-filled, scores
@@ -625,7 +631,11 @@ __global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_kernel(const __grid_con
 }
 
 // Requests of at most kFewRows rows (query heads of one key head x tokens) go to
-// this file's kernel, larger ones to kv4_attention_tc.cu.
+// this file's kernel, larger ones to kv4_attention_tc.cu.  Both measured, us at
+// 32 / 64 / 96 / 128 rows a request, 8 key heads, D = 128: one request of 4096
+// keys 14.8 / 19.6 / 28.3 / 27.5 here, 20.4 / 20.6 / 21.0 / 23.6 there; 16 of
+// them 53 / 86 / 124 / 153 and 79 / 81 / 83 / 86 (D = 64: 35 / 57 / 79 / 98 and
+// 63 / 64 / 66 / 68).
 constexpr int kFewRows = 64, kFewRowsInAll = 512;
 
 size_t parts_bytes(const Kv4AttnLaunch& p) {
@@ -708,11 +718,11 @@ Kv4Plan kv4_attention_plan(const Kv4AttnLaunch& base, int max_kv, int num_sms) {
   }
   // The smallest tile that holds an average request's rows: a larger one
   // dequantizes each key for more rows at once, a smaller one leaves room for
-  // more warps.
-  // Unequal requests (q_start): half as much again, so that most still fit one
-  // tile; beside prompts, single tokens.
+  // more warps (20 rows, 16 x 3001 keys, 8 heads: tiles of 24 rows 35.1 us, of
+  // 32 42.8; D = 64: 26.0 and 29.8).
+  // Beside prompts (q_start), single tokens.
   long long each = base.requests > 0 ? (rows + base.requests - 1) / base.requests : 0;
-  if (base.q_start) each = plan.use_many ? base.q_heads / base.c.heads : each + each / 2;
+  if (base.q_start && plan.use_many) each = base.q_heads / base.c.heads;
   const int nt = each <= 8 ? 1 : each <= 16 ? 2 : each <= 24 ? 3 : 4;
   plan_launch(plan.few, 8 * nt, 0, plan.use_many ? kFewRows : kAll, (long long)num_sms * ctas_per_sm(base.c.D, nt), max_kv);
   plan_launch(plan.many, 256, plan.use_few ? kFewRows + 1 : 0, kAll, num_sms, max_kv);
