@@ -91,18 +91,24 @@ struct RowsArgs {
   int tb, hb;                                   // tokens and heads per CTA
 };
 
-// BF16: storage type.  LOGLP: log2 of the lanes per row.
-template <bool BF16, int LOGLP>
+// Where a pair's halves are: neighbours, this lane's two chunks (half-split pairs over the whole of a head of 16 LP
+// values), or two chunks anywhere.
+enum Pairs { kAdjacent, kOwnChunks, kAnyChunks };
+
+// BF16: storage type.  LOGLP: log2 of the lanes per row.  HAD: with the Hadamard step.
+template <bool BF16, int LOGLP, Pairs PAIRS, bool HAD>
 __global__ void __launch_bounds__(kThreadsR, kCtasR) qk_norm_rope_kernel(const __grid_constant__ RowsArgs a) {
   constexpr int LP = 1 << LOGLP, kSlots = kThreadsR / LP;
-  // Of token t and pair j: cos and sin, adjacent for adjacent pairs, in two halves of the table otherwise.
+  // Of each token's pairs: cos and sin, adjacent for adjacent pairs, in two halves of the table otherwise.  A lane reads
+  // what belongs to one chunk as two 16-byte pieces; all chunks' first pieces come first, then all second ones, so that
+  // neighbours read neighbouring words.
   __shared__ __align__(16) float table[2 * kMaxTable];
-  __shared__ __align__(16) float gain[2][16 * LP];        // norm weights of queries and keys
+  __shared__ __align__(16) float gain[2][16 * LP];        // norm weights of queries and keys, in such pieces too
   const QkNormRopeLaunch& p = a.p;
-  const int D = p.D, P = p.pairs, chunks = D / 8;
+  const int D = p.D, P = p.pairs, PT = (P + 3) & ~3, chunks = D / 8;
   const int t0 = blockIdx.x * a.tb, nt = min(a.tb, p.tokens - t0);
   const int slot = threadIdx.x / LP, l = threadIdx.x % LP;
-  const bool inter = p.interleaved, whole = chunks == 2 * LP && 2 * P == D;       // every lane full, every pair rotated
+  constexpr bool inter = PAIRS == kAdjacent;
   const float inv_d = 1.0f / (float)D;
 
   griddep_wait();
@@ -111,7 +117,8 @@ __global__ void __launch_bounds__(kThreadsR, kCtasR) qk_norm_rope_kernel(const _
     const uint16_t* g = static_cast<const uint16_t*>(i < D ? p.q.weight : p.k.weight);
     if (g) {
       const uint16_t bits = g[i < D ? i : i - D];
-      gain[i >= D][i < D ? i : i - D] =
+      const int d = i < D ? i : i - D;
+      gain[i >= D][(d >> 2 & 1) * (8 * LP) + 4 * (d >> 3) + (d & 3)] =
           BF16 ? __uint_as_float((uint32_t)bits << 16) : __half2float(__ushort_as_half(bits));
     }
   }
@@ -153,8 +160,15 @@ __global__ void __launch_bounds__(kThreadsR, kCtasR) qk_norm_rope_kernel(const _
         angle -= rint(angle);
         float sn, cn;
         sincospif(2.0f * (float)angle, &sn, &cn);
-        table[inter ? 2 * i : i] = cn;
-        table[inter ? 2 * i + 1 : kMaxTable + i] = sn;
+        if (inter) {
+          float* e = table + 2 * (tt * PT) + (j >> 1 & 1) * PT + 4 * (j >> 2) + 2 * (j & 1);
+          e[0] = cn;
+          e[1] = sn;
+        } else {
+          float* e = table + tt * P + (j >> 2 & 1) * (P / 2) + 4 * (j >> 3) + (j & 3);
+          e[0] = cn;
+          e[kMaxTable] = sn;
+        }
       }
       __syncthreads();
     }
@@ -182,10 +196,10 @@ __global__ void __launch_bounds__(kThreadsR, kCtasR) qk_norm_rope_kernel(const _
       const uint64_t rs2 = pk2(rs, rs);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float* g = gain[side] + 8 * (l + LP * c);   // (16 LP of them: in range for lanes without a chunk too)
+        const float* g = gain[side] + 4 * (l + LP * c);   // (16 LP of them: in range for lanes without a chunk too)
         uint64_t g2[4];
         load2(g, g2[0], g2[1]);
-        load2(g + 4, g2[2], g2[3]);
+        load2(g + 8 * LP, g2[2], g2[3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[c][i] = mul2(mul2(v[c][i], rs2), g2[i]);
       }
@@ -196,27 +210,27 @@ __global__ void __launch_bounds__(kThreadsR, kCtasR) qk_norm_rope_kernel(const _
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int p0 = 4 * (l + LP * c);
-          const float* e = table + 2 * (tl * P + p0);
-          if (whole || (p0 + 4 <= P && (P & 1) == 0)) {   // cos and sin of two pairs at once, 16-byte aligned
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              const float4 cs = *reinterpret_cast<const float4*>(e + 2 * i);
-              turn(v[c][i], cs.x, cs.y);
-              turn(v[c][i + 1], cs.z, cs.w);
+          const float* e = table + 2 * (tl * PT) + p0;
+          if (p0 < P) {                                   // cos and sin of two pairs at once
+            const float4 e0 = *reinterpret_cast<const float4*>(e), e1 = *reinterpret_cast<const float4*>(e + PT);
+            turn(v[c][0], e0.x, e0.y);
+            if (p0 + 4 <= P) {
+              turn(v[c][1], e0.z, e0.w);
+              turn(v[c][2], e1.x, e1.y);
+              turn(v[c][3], e1.z, e1.w);
+            } else {
+              if (p0 + 1 < P) turn(v[c][1], e0.z, e0.w);
+              if (p0 + 2 < P) turn(v[c][2], e1.x, e1.y);
             }
-          } else if (p0 < P) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (p0 + i < P) turn(v[c][i], e[2 * i], e[2 * i + 1]);
           }
         }
-      } else if (P == 8 * LP) {                      // the pair's halves are this lane's two chunks
-        const float* e = table + tl * P + 8 * l;
+      } else if (PAIRS == kOwnChunks) {
+        const float* e = table + tl * P + 4 * l;
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
           uint64_t cn[2], sn[2];
-          load2(e + 2 * i, cn[0], cn[1]);
-          load2(e + kMaxTable + 2 * i, sn[0], sn[1]);
+          load2(e + (i / 2) * (P / 2), cn[0], cn[1]);
+          load2(e + kMaxTable + (i / 2) * (P / 2), sn[0], sn[1]);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const uint64_t x0 = v[0][i + q], x1 = v[1][i + q];
@@ -243,12 +257,12 @@ __global__ void __launch_bounds__(kThreadsR, kCtasR) qk_norm_rope_kernel(const _
           const int ci = l + LP * c;
           if (ci < 2 * pc) {
             const bool first = ci < pc;
-            const float* e = table + tl * P + 8 * (first ? ci : ci - pc);
+            const float* e = table + tl * P + 4 * (first ? ci : ci - pc);
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
               uint64_t cn[2], sn[2];
-              load2(e + 2 * i, cn[0], cn[1]);
-              load2(e + kMaxTable + 2 * i, sn[0], sn[1]);
+              load2(e + (i / 2) * (P / 2), cn[0], cn[1]);
+              load2(e + kMaxTable + (i / 2) * (P / 2), sn[0], sn[1]);
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
                 const uint64_t x = v[c][i + q], y = o[c][i + q];
@@ -260,7 +274,7 @@ __global__ void __launch_bounds__(kThreadsR, kCtasR) qk_norm_rope_kernel(const _
       }
     }
 
-    if (p.hadamard) {                                // D is a power of two; D = 8 has one chunk (LP = 1)
+    if (HAD) {                                       // D is a power of two; D = 8 has one chunk (LP = 1)
       const bool two = D >= 16;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -315,7 +329,7 @@ __global__ void __launch_bounds__(kThreadsR, kCtasR) qk_norm_rope_kernel(const _
   }
 }
 
-template <bool BF16, int LOGLP>
+template <bool BF16, int LOGLP, Pairs PAIRS, bool HAD>
 cudaError_t launch(const QkNormRopeLaunch& p, cudaStream_t stream) {
   constexpr int kSlots = kThreadsR >> LOGLP;
   const int heads = p.q.heads + p.k.heads;
@@ -329,12 +343,15 @@ cudaError_t launch(const QkNormRopeLaunch& p, cudaStream_t stream) {
     a.tb = heads >= kSlots ? 1 : kSlots / heads;
     a.hb = kSlots < heads ? kSlots : heads;
   } else {
-    const int most = p.pairs > 0 ? kMaxTable / p.pairs : kMaxTable;
+    const int most = p.pairs > 0 ? kMaxTable / ((p.pairs + 3) & ~3) : kMaxTable;
     const long long share = (p.tokens + resident - 1) / resident, rounds = (share + most - 1) / most;
     a.tb = (int)((p.tokens + resident * rounds - 1) / (resident * rounds));
     a.hb = heads;
   }
-  if (p.pairs > 0 && a.tb > kMaxTable / p.pairs) a.tb = kMaxTable / p.pairs;    // pairs <= 128
+  if (p.pairs > 0) {                            // at most 128 of them
+    const int most = kMaxTable / ((p.pairs + 3) & ~3);
+    if (a.tb > most) a.tb = most;
+  }
   const dim3 grid((unsigned)((p.tokens + a.tb - 1) / a.tb), (unsigned)((heads + a.hb - 1) / a.hb));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -345,16 +362,28 @@ cudaError_t launch(const QkNormRopeLaunch& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<BF16, LOGLP>, a);
+  return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<BF16, LOGLP, PAIRS, HAD>, a);
+}
+
+template <bool BF16, int LOGLP>
+cudaError_t launch_kind(const QkNormRopeLaunch& p, cudaStream_t stream) {
+  const Pairs pairs = p.interleaved ? kAdjacent : p.pairs == (8 << LOGLP) ? kOwnChunks : kAnyChunks;
+  if (p.hadamard)
+    return pairs == kAdjacent    ? launch<BF16, LOGLP, kAdjacent, true>(p, stream)
+           : pairs == kOwnChunks ? launch<BF16, LOGLP, kOwnChunks, true>(p, stream)
+                                 : launch<BF16, LOGLP, kAnyChunks, true>(p, stream);
+  return pairs == kAdjacent    ? launch<BF16, LOGLP, kAdjacent, false>(p, stream)
+         : pairs == kOwnChunks ? launch<BF16, LOGLP, kOwnChunks, false>(p, stream)
+                               : launch<BF16, LOGLP, kAnyChunks, false>(p, stream);
 }
 
 template <bool BF16>
 cudaError_t launch_lp(const QkNormRopeLaunch& p, cudaStream_t stream) {
-  if (p.D <= 16) return launch<BF16, 0>(p, stream);
-  if (p.D <= 32) return launch<BF16, 1>(p, stream);
-  if (p.D <= 64) return launch<BF16, 2>(p, stream);
-  if (p.D <= 128) return launch<BF16, 3>(p, stream);
-  return launch<BF16, 4>(p, stream);
+  if (p.D <= 16) return launch_kind<BF16, 0>(p, stream);
+  if (p.D <= 32) return launch_kind<BF16, 1>(p, stream);
+  if (p.D <= 64) return launch_kind<BF16, 2>(p, stream);
+  if (p.D <= 128) return launch_kind<BF16, 3>(p, stream);
+  return launch_kind<BF16, 4>(p, stream);
 }
 
 }  // namespace
