@@ -164,7 +164,7 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, q_weight: Op
     q (tokens, q_heads, head_dim), k (tokens, k_heads, head_dim) or None; weights (head_dim,); positions
     (tokens,) or (tokens, axes) int32; inv_freq (pairs,) fp32; pair_axis (pairs,) uint8, the axis of each pair
     (None: axis 0); pairs are adjacent channels if ``interleaved``, else channels p and p + pairs.  Returns
-    (q, k), new and contiguous, or the arguments themselves if ``inplace``.
+    (q, k), new and contiguous, or the arguments themselves, written over, if ``inplace``.
     """
     return _run((_native or _calls()).qk_norm_rope, "svdq_qk_norm_rope", q, stream, q, k, q_weight, k_weight, eps, positions,
                 inv_freq, pair_axis, interleaved, hadamard, inplace)
@@ -216,7 +216,7 @@ def kv4_attention(q: torch.Tensor, cache, kv_len: torch.Tensor, block_table: tor
     Request b has kv_len[b] keys (int32, the new tokens' own among them), key j in page block_table[b, j //
     page_size] (int32, (requests, max_pages)); its queries are tokens q_start[b] .. q_start[b + 1] (int32,
     (requests + 1,), ascending; None: the same number each) and stand at its last positions.  causal: a query
-    sees keys up to its own position, else all.  softmax_scale defaults to 1 / sqrt(head_dim).  max_kv_len, an
+    sees keys up to its own position, else all.  out may not overlap q.  softmax_scale defaults to 1 / sqrt(head_dim).  max_kv_len, an
     upper bound of kv_len known to the caller, only steers how the work is split.
 
     Returns out (tokens, q_heads, head_dim), with ``return_lse`` also the log sums (tokens, q_heads) fp32.  A

@@ -4,7 +4,7 @@
 //
 // A CPython extension module rather than ctypes calls: at single tokens a kernel
 // takes 2 to 8 us, and the same checks and descriptions in Python took 7 to 9 us
-// a call (norms 14 us a call, of which 4 are the launch; here about 7).
+// a call (norms 14 us a call, of which 4 are the launch; here 6).
 // attention.py documents the arguments; everything here is positional, and a
 // `stream` argument has been made current by then.
 #include <c10/cuda/CUDAGuard.h>
@@ -12,6 +12,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/MemoryOverlap.h>
 
 #include <cmath>
 #include <cstdarg>
@@ -104,6 +105,13 @@ void distinct(const at::Tensor& t, const char* name) {
     if (t.stride(i) < extent) raise(PyExc_ValueError, "%s: its elements overlap in memory", name);
     extent += t.stride(i) * (t.size(i) - 1);
   }
+}
+// Refuses an output that lies over another argument (views of one buffer side by side are fine).
+void apart(const at::Tensor& t, const char* name, const at::Tensor& other, const char* other_name) {
+  if (t.numel() == 0 || other.numel() == 0 || !t.is_alias_of(other)) return;
+  const auto status = at::get_overlap_status(t, other);
+  if (status == at::MemOverlapStatus::Full || status == at::MemOverlapStatus::Partial || t.data_ptr() == other.data_ptr())
+    raise(PyExc_ValueError, "%s and %s overlap in memory", name, other_name);
 }
 // A contiguous vector of n elements (n < 0: any number).
 const at::Tensor& vector(PyObject* o, const char* name, at::ScalarType type, int64_t n, int* device) {
@@ -249,7 +257,10 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
     if (truth(a[10])) {
       distinct(q, "q");
-      if (k) distinct(*k, "k");
+      if (k) {
+        distinct(*k, "k");
+        apart(q, "q", *k, "k");
+      }
       d.q_out = d.q;
       d.k_out = d.k;
       return answer(svdq_qk_norm_rope(&d, current_stream(device)), PyTuple_Pack(2, a[0], a[1]));
@@ -344,6 +355,7 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       need_shape(out, "out", q.size(0), q.size(1), q.size(2));
       d.out = heads_of(out, "out");
       distinct(out, "out");
+      apart(out, "out", q, "q");
     } else {
       out = empty(q.sizes(), q, q.scalar_type());
       d.out = contiguous_heads(out);

@@ -550,81 +550,81 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
   } else {
     set_registers<false, 72>();
     if (warp == 12) {
-    // ------------------------------------------------------------ MMA
-    constexpr uint32_t kIdS = idesc_f16(kHalf, kKeys, false), kIdO = idesc_f16(kHalf, D, true);
-    bool ok = true;
-    uint32_t n_all = 0, n_tile[2] = {0, 0}, n_job[2] = {0, 0};      // tiles of the CTA, tiles and segments of each half
-    // Operand descriptors of half 0, stage 0: an offset only adds to the low word (address / 16).  The loop below is one
-    // thread's instruction stream beside MMAs of 64 cycles, so everything that can be is a constant there.
-    const uint64_t q_desc = sdesc_kmajor_sw128(base + SM::kQ), k_desc = sdesc_kmajor_sw128(base + SM::kK),
-                   v_desc = sdesc_mnmajor_sw128(base + SM::kV, kKeys * 128);
-    const uint32_t one = elect_one(), tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    auto segment = [&](auto halves, int tiles) {
-      constexpr int H = decltype(halves)::value;
-      auto scores = [&](int h, uint64_t k) {
+      // ------------------------------------------------------------ MMA
+      constexpr uint32_t kIdS = idesc_f16(kHalf, kKeys, false), kIdO = idesc_f16(kHalf, D, true);
+      bool ok = true;
+      uint32_t n_all = 0, n_tile[2] = {0, 0}, n_job[2] = {0, 0};      // tiles of the CTA, tiles and segments of each half
+      // Operand descriptors of half 0, stage 0: an offset only adds to the low word (address / 16).  The loop below is one
+      // thread's instruction stream beside MMAs of 64 cycles, so everything that can be is a constant there.
+      const uint64_t q_desc = sdesc_kmajor_sw128(base + SM::kQ), k_desc = sdesc_kmajor_sw128(base + SM::kK),
+                     v_desc = sdesc_mnmajor_sw128(base + SM::kV, kKeys * 128);
+      const uint32_t one = elect_one(), tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      auto segment = [&](auto halves, int tiles) {
+        constexpr int H = decltype(halves)::value;
+        auto scores = [&](int h, uint64_t k) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = ((i / 4) * (kKeys * 128) + (i % 4) * 32) >> 4;
-          mma_f16_ss(one, tm + h * kKeys, q_desc + (h * (SM::kTile >> 4) + off), k + off, kIdS, i > 0);
-        }
-        commit_one(one, ctl.bar(kSFull + h));
-      };
-      auto outputs = [&](int h, int x, uint64_t v, uint32_t accumulate) {
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = ((i / 4) * (kKeys * 128) + (i % 4) * 32) >> 4;
+            mma_f16_ss(one, tm + h * kKeys, q_desc + (h * (SM::kTile >> 4) + off), k + off, kIdS, i > 0);
+          }
+          commit_one(one, ctl.bar(kSFull + h));
+        };
+        auto outputs = [&](int h, int x, uint64_t v, uint32_t accumulate) {
 #pragma unroll
-        for (int i = 4 * x; i < 4 * x + 4; ++i)
-          mma_f16_ts(one, tm + 2 * kKeys + h * D, tm + h * kKeys + 64 + 8 * i, v + (i * 2048 >> 4), kIdO,
-                     i > 4 * x ? 1u : accumulate);
-      };
-      ok = ctl.wait_warp(kKFull + (n_all & 1), n_all >> 1);
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        ok = ok && ctl.wait_warp(kQFull + h, n_job[h]++);
-        if (!ok) return;
-        tc_fence_after_sync();
-        scores(h, k_desc + (n_all & 1) * (SM::kTile >> 4));
-      }
-      commit_one(one, ctl.bar(kKFree + (n_all & 1)));
-      // Tile by tile, for each half in turn: outputs of its two parts as they come, then the next tile's scores in the
-      // columns that these weights leave.  The scores' commit stands for the outputs too (MMAs end in order); the last
-      // tile's outputs have their own.
-      for (int left = tiles; left > 0; --left) {
-        const uint32_t so = n_all & 1, ss = so ^ 1u;
-        const uint64_t v = v_desc + so * (SM::kTile >> 4), k = k_desc + ss * (SM::kTile >> 4);
-        ok = ctl.wait_warp(kVFull + so, n_all >> 1);
-        ++n_all;
+          for (int i = 4 * x; i < 4 * x + 4; ++i)
+            mma_f16_ts(one, tm + 2 * kKeys + h * D, tm + h * kKeys + 64 + 8 * i, v + (i * 2048 >> 4), kIdO,
+                       i > 4 * x ? 1u : accumulate);
+        };
+        ok = ctl.wait_warp(kKFull + (n_all & 1), n_all >> 1);
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-          ok = ok && ctl.wait_warp(kPFull + 2 * h + 1, n_tile[h]);
+          ok = ok && ctl.wait_warp(kQFull + h, n_job[h]++);
           if (!ok) return;
           tc_fence_after_sync();
-          outputs(h, 1, v, left < tiles ? 1u : 0u);
-          ok = ctl.wait_warp(kPFull + 2 * h, n_tile[h]++);
-          if (ok && left > 1 && h == 0) ok = ctl.wait_warp(kKFull + ss, n_all >> 1);
-          if (!ok) return;
-          tc_fence_after_sync();
-          outputs(h, 0, v, 1u);
-          if (h == H - 1) commit_one(one, ctl.bar(kVFree + so));
-          if (left > 1)
-            scores(h, k);
-          else
-            commit_one(one, ctl.bar(kOFull + h));
+          scores(h, k_desc + (n_all & 1) * (SM::kTile >> 4));
         }
-        if (left > 1) commit_one(one, ctl.bar(kKFree + ss));
+        commit_one(one, ctl.bar(kKFree + (n_all & 1)));
+        // Tile by tile, for each half in turn: outputs of its two parts as they come, then the next tile's scores in the
+        // columns that these weights leave.  The scores' commit stands for the outputs too (MMAs end in order); the last
+        // tile's outputs have their own.
+        for (int left = tiles; left > 0; --left) {
+          const uint32_t so = n_all & 1, ss = so ^ 1u;
+          const uint64_t v = v_desc + so * (SM::kTile >> 4), k = k_desc + ss * (SM::kTile >> 4);
+          ok = ctl.wait_warp(kVFull + so, n_all >> 1);
+          ++n_all;
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            ok = ok && ctl.wait_warp(kPFull + 2 * h + 1, n_tile[h]);
+            if (!ok) return;
+            tc_fence_after_sync();
+            outputs(h, 1, v, left < tiles ? 1u : 0u);
+            ok = ctl.wait_warp(kPFull + 2 * h, n_tile[h]++);
+            if (ok && left > 1 && h == 0) ok = ctl.wait_warp(kKFull + ss, n_all >> 1);
+            if (!ok) return;
+            tc_fence_after_sync();
+            outputs(h, 0, v, 1u);
+            if (h == H - 1) commit_one(one, ctl.bar(kVFree + so));
+            if (left > 1)
+              scores(h, k);
+            else
+              commit_one(one, ctl.bar(kOFull + h));
+          }
+          if (left > 1) commit_one(one, ctl.bar(kKFree + ss));
+        }
+      };
+      for (long long u = u0; ok && u < u1;) {
+        const Job job = next_job(w, wu, u, u0, u1);
+        u += job.tiles;
+        const int tiles = __shfl_sync(0xFFFFFFFFu, job.tiles, 0);
+        if (__shfl_sync(0xFFFFFFFFu, job.halves, 0) == 2)
+          segment(std::integral_constant<int, 2>(), tiles);
+        else
+          segment(std::integral_constant<int, 1>(), tiles);
       }
-    };
-    for (long long u = u0; ok && u < u1;) {
-      const Job job = next_job(w, wu, u, u0, u1);
-      u += job.tiles;
-      const int tiles = __shfl_sync(0xFFFFFFFFu, job.tiles, 0);
-      if (__shfl_sync(0xFFFFFFFFu, job.halves, 0) == 2)
-        segment(std::integral_constant<int, 2>(), tiles);
-      else
-        segment(std::integral_constant<int, 1>(), tiles);
-    }
-    // Whatever ended the roles: the MMAs that were issued end before the memory they use is given up.
-    commit_one(one, ctl.bar(kEnd));
-    if (one) wait_for(ctl.bar(kEnd), 0, kWaitTimeoutNs);
-    __syncwarp();
+      // Whatever ended the roles: the MMAs that were issued end before the memory they use is given up.
+      commit_one(one, ctl.bar(kEnd));
+      if (one) wait_for(ctl.bar(kEnd), 0, kWaitTimeoutNs);
+      __syncwarp();
     }
   }
   tc_fence_before_sync();

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import bit_quantized_linear_svdq_b200 as S
-from bit_quantized_linear_svdq_b200 import synthetic
+from bit_quantized_linear_svdq_b200 import attention, synthetic
 from oracle import svdq_oracle as O
 
 pytestmark = pytest.mark.gpu
@@ -89,6 +89,11 @@ ROPE_CASES = [
     (6, 7, 3, 128, BF, (), True, False, False, True),             # rotation alone
     (3000, 8, 2, 128, BF, (64,), True, False, True, False),       # many tokens a CTA
     (2500, 1, 1, 256, BF, (128,), True, True, True, True),
+    (70, 3, 1, 128, FP, (32,), True, False, True, True),          # half-split pairs of a quarter of the head, rotated
+    (1700, 2, 1, 64, BF, (8,), True, False, True, True),
+    (300, 2, 2, 40, FP, (13,), True, True, True, False),          # adjacent pairs that end inside a chunk
+    (4500, 1, 1, 64, BF, (3, 2), True, True, True, True),
+    (21, 2, 2, 32, FP, (5, 5, 5), True, True, False, False),
 ]
 
 
@@ -229,6 +234,29 @@ def test_append_and_read(t, h, d, page, dtype):
         want = torch.from_numpy(np.asarray(O.dequantize_nvfp4(*rows))).reshape(-1, h, d)
         assert torch.equal(got[~skipped].double().nan_to_num(nan=7e4), want.double().nan_to_num(nan=7e4))
         assert (got[skipped] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_at_any_16_bytes(d, dtype):
+    """Rows that start at odd multiples of 16 bytes, read by append and written by the C entry point of read."""
+    g = gen(17)
+    t, h = 45, 3
+    wide = torch.randn(2, t, h, d + 8, device="cuda", generator=g).to(dtype)
+    k, v = wide[0, ..., 8:], wide[1, ..., :d]
+    slots = torch.randperm(64, device="cuda", generator=g)[:t]
+    a, b = S.kv4_cache(4, 16, h, d), S.kv4_cache(4, 16, h, d)
+    S.kv4_append(a, k, v, slots)
+    S.kv4_append(b, k.contiguous(), v.contiguous(), slots)
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and a.k_codes.any()
+    want = S.kv4_read(a, slots, dtype)
+    out = torch.full_like(wide, 7.0)
+    side = [attention.svdq_heads(o.data_ptr(), o.stride(0), o.stride(1)) for o in (out[0, ..., 8:], out[1, ..., :d])]
+    c = attention.svdq_kv4_cache(*(x.data_ptr() for x in a), 4, h, 16, d)
+    attention.svdq_kv4_read(c, *side, t, 0 if dtype is BF else 1, slots.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0, ..., 8:], want[0]) and torch.equal(out[1, ..., :d], want[1])
+    assert (out[0, ..., :8] == 7).all() and (out[1, ..., d:] == 7).all()
 
 
 def test_append_matches_the_weight_quantizer():
@@ -583,7 +611,39 @@ def test_attention_refusals():
             call()
 
 
+def test_outputs_over_inputs_are_refused():
+    case = ([64, 32], 2, 4, 2, 64, 16, True, BF)
+    q, cache, lens, table, start, causal = make(case, 62)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = S.kv4_attention(q, cache, n, table)
+    room = torch.zeros(6, 4, 64, dtype=BF, device="cuda")
+    room[:4] = q
+    for out in (room[:4], room[1:5], room[2:]):
+        with pytest.raises(ValueError, match="overlap"):
+            S.kv4_attention(room[:4], cache, n, table, out=out)
+    both = torch.cat((q, torch.zeros_like(q)), 1)                # heads of one buffer, side by side
+    assert S.kv4_attention(both[:, :4], cache, n, table, out=both[:, 4:]).data_ptr() == both[:, 4:].data_ptr()
+    assert torch.equal(both[:, 4:], want) and torch.equal(both[:, :4], q)
+    with pytest.raises(ValueError, match="overlap"):
+        S.qk_norm_rope(q, q, torch.ones(64, dtype=BF, device="cuda"), inplace=True)
+
+
 # ------------------------------------------------------------------ streams, graphs, and a run of them together
+
+def test_calls_at_once_on_two_streams():
+    calls = []
+    for i, case in enumerate([([900, 1500], 256, 8, 2, 128, 64, True, BF), ([3000, 40], 1, 8, 2, 128, 64, True, BF),
+                              ([700], 300, 4, 4, 64, 32, True, FP)]):
+        q, cache, lens, table, start, causal = make(case, 90 + i)
+        n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        calls.append((q, cache, n, table))
+    want = [S.kv4_attention(*c) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [S.kv4_attention(*calls[(i + j) % 3], stream=streams[j]) for i in range(12) for j in range(2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[2 * i + j], want[(i + j) % 3]) for i in range(12) for j in range(2))
+
 
 def test_streams_and_graphs():
     case = ([900, 40], 1, 8, 2, 128, 64, True, BF)
