@@ -630,6 +630,87 @@ __global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_kernel(const __grid_con
   }
 }
 
+// The same for tiles of 256 rows, mostly in two or three parts: a warp takes two
+// rows of a note, two parts of each in flight.  After the prompt chunks that
+// kv4_attention_tc.cu measures (147 notes, about 40 MB of parts) this takes 12
+// us, the kernel above 28, four rows a warp 17, one 14.
+constexpr int kRowsJ = 2;
+template <int D, bool BF16>
+__global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_rows_kernel(const __grid_constant__ Kv4AttnLaunch p) {
+  constexpr int kVec = D / 32, kFlight = 2;
+  __shared__ float acc[kWarpsJ][kRowsJ][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = p.q_heads / p.c.heads;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int per_cut = p.tile_rows / kRowsJ, items = (p.ctas - 1) * per_cut;
+  for (int i = blockIdx.x * kWarpsJ + warp; i < items; i += gridDim.x * kWarpsJ) {
+    const int c0 = i / per_cut, r0 = (i - c0 * per_cut) * kRowsJ;
+    const Kv4Cut cut = p.cuts[c0];
+    const int rows = min(cut.rows - r0, kRowsJ);
+    if (rows <= 0) continue;
+    float top[kRowsJ], total[kRowsJ], v[kRowsJ][kVec];
+#pragma unroll
+    for (int r = 0; r < kRowsJ; ++r) {
+      top[r] = -INFINITY, total[r] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[r][j] = 0.0f;
+    }
+    for (int c = c0; c <= cut.last_cta; c += kFlight) {
+      float2 ml[kFlight][kRowsJ];
+      float a[kFlight][kRowsJ][kVec];
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q)
+#pragma unroll
+        for (int r = 0; r < kRowsJ; ++r) {
+          ml[q][r] = make_float2(-INFINITY, 0.0f);
+          if (c + q <= cut.last_cta && r < rows) {
+            const long long at = (2ll * (c + q) + (c + q == c0 ? cut.slot : 0)) * p.tile_rows + r0 + r;
+            const float* src = p.part_o + at * D + kVec * lane;
+            ml[q][r] = p.part_ml[at];
+            if (kVec == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(src);
+              a[q][r][0] = x.x, a[q][r][1] = x.y, a[q][r][kVec - 2] = x.z, a[q][r][kVec - 1] = x.w;
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(src);
+              a[q][r][0] = x.x, a[q][r][1] = x.y;
+            }
+          }
+        }
+#pragma unroll
+      for (int r = 0; r < kRowsJ; ++r) {
+        const float to = fmaxf(top[r], fmaxf(ml[0][r].x, ml[1][r].x)), f0 = ex2_diff(top[r], to);
+        top[r] = to;
+        total[r] *= f0;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[r][j] *= f0;
+#pragma unroll
+        for (int q = 0; q < kFlight; ++q)
+          if (c + q <= cut.last_cta && r < rows) {
+            const float f = ex2_diff(ml[q][r].x, to);
+            total[r] = fmaf(ml[q][r].y, f, total[r]);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) v[r][j] = fmaf(a[q][r][j], f, v[r][j]);
+          }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRowsJ; ++r)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) acc[warp][r][kVec * lane + j] = v[r][j];
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < kRowsJ; ++r)
+      if (r < rows && lane < D / 8) {
+        const int row = cut.row0 + r0 + r, tok = row / group, head = cut.head * group + row - tok * group;
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = acc[warp][r][8 * lane + j];
+        store_row8<BF16>(p, cut.token0 + tok, head, 8 * lane, y, top[r], total[r]);
+      }
+    __syncwarp();
+  }
+}
+
 // Requests of at most kFewRows rows (query heads of one key head x tokens) go to
 // this file's kernel, larger ones to kv4_attention_tc.cu.  Both measured, us at
 // 32 / 64 / 96 / 128 rows a request, 8 key heads, D = 128: one request of 4096
@@ -661,6 +742,10 @@ cudaError_t launch_join(const Kv4AttnLaunch& p, cudaStream_t stream) {
   if (p.ctas > 8 * p.segments)
     return launch_after(kv4_join_kernel<D, kWarpsJ, BF16>, dim3((unsigned)(p.ctas + 31) / 32, (unsigned)p.tile_rows),
                         32 * kWarpsJ, 0, stream, p);
+  if (p.tile_rows > 32) {
+    const int items = (p.ctas - 1) * (p.tile_rows / kRowsJ);
+    return launch_after(kv4_join_rows_kernel<D, BF16>, dim3((unsigned)(items + kWarpsJ - 1) / kWarpsJ), 32 * kWarpsJ, 0, stream, p);
+  }
   const long long blocks = ((long long)(p.ctas - 1) * p.tile_rows + kWarpsJ - 1) / kWarpsJ, most = 16ll * p.num_sms;
   return launch_after(kv4_join_kernel<D, 1, BF16>, dim3((unsigned)(blocks < most ? blocks : most)), 32 * kWarpsJ, 0, stream, p);
 }

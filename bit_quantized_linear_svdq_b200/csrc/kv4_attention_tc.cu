@@ -6,9 +6,10 @@
 // value is dequantized once for 256 rows.  At that many rows the products
 // bound it (4 D flops a row and key: D = 128, 2048 cycles a tile), and next to
 // them the exponentials (one a row and key: as many cycles of the special
-// function unit).  Measured about 3900 cycles a tile, 0.82 PFLOP/s on chunks of
-// up to 1024 tokens behind 8203 keys and 0.92 on 4096 queries of 32 heads over
-// 4333 keys (0.5 and 0.56 of the measured bf16 rate): a half's chain from scores
+// function unit).  Measured about 3900 cycles a tile; with the join 0.88 PFLOP/s
+// on chunks of up to 1024 tokens behind 8203 keys (216 us) and 0.97 on 4096
+// queries of 32 heads over 4333 keys (300 us), 0.54 and 0.59 of the measured bf16
+// rate: a half's chain from scores
 // to weights and back through its two products is not hidden altogether by the
 // other half's.
 //
@@ -16,7 +17,7 @@
 //   warps 0-3, 4-7   softmax of half 0 and 1: thread = row = tensor memory lane.
 //                    A row's 128 scores come from tensor memory into registers
 //                    (with 152 registers and half of them read twice: 266 us
-//                    against 231), weights go back there as fp16 over the
+//                    against 231, join and all, at the time), weights go back there as fp16 over the
 //                    scores; the output is rescaled there only when the
 //                    reference exponent rises by more than 8.
 //   warps 8-11       thread = key of the tile: 4-bit rows -> fp16 rows in shared
@@ -28,7 +29,7 @@
 //                    turn, so that one half's softmax runs beside the other's
 //                    products; each half's outputs begin with the first 64
 //                    weights a row.
-// Measured and left out (the prompt chunks above, 231 us): 64-key sub-tiles with
+// Measured and left out (the prompt chunks above, then 231 us): 64-key sub-tiles with
 // scores double-buffered (an MMA of N = 64 takes 48 cycles, not 32: 302 us
 // against 284 at the time); two threads a row on 16 warps (284 against 275); an
 // eighth to a half of the exponentials as polynomials on the FMA pipe (235 to 280
