@@ -9,17 +9,16 @@
 // function unit).  Measured about 3900 cycles a tile; with the join 0.88 PFLOP/s
 // on chunks of up to 1024 tokens behind 8203 keys (216 us) and 0.97 on 4096
 // queries of 32 heads over 4333 keys (300 us), 0.54 and 0.59 of the measured bf16
-// rate: a half's chain from scores
-// to weights and back through its two products is not hidden altogether by the
-// other half's.
+// rate: a half's chain from scores to weights and back through its two products is
+// not hidden altogether by the other half's.
 //
 // Roles (one CTA per SM; 176, 176, 88 and 72 registers a thread):
 //   warps 0-3, 4-7   softmax of half 0 and 1: thread = row = tensor memory lane.
 //                    A row's 128 scores come from tensor memory into registers
 //                    (with 152 registers and half of them read twice: 266 us
-//                    against 231, join and all, at the time), weights go back there as fp16 over the
-//                    scores; the output is rescaled there only when the
-//                    reference exponent rises by more than 8.
+//                    against 231 at the time), weights go back there as fp16
+//                    over the scores; the output is rescaled there only when
+//                    the reference exponent rises by more than 8.
 //   warps 8-11       thread = key of the tile: 4-bit rows -> fp16 rows in shared
 //                    memory, K and V in the same layout (128-byte swizzled rows
 //                    of 64 dims): K is the first product's K-major operand, V
@@ -29,11 +28,13 @@
 //                    turn, so that one half's softmax runs beside the other's
 //                    products; each half's outputs begin with the first 64
 //                    weights a row.
-// Measured and left out (the prompt chunks above, then 231 us): 64-key sub-tiles with
-// scores double-buffered (an MMA of N = 64 takes 48 cycles, not 32: 302 us
+// Measured and left out (the prompt chunks above, then 231 us): 64-key sub-tiles
+// with scores double-buffered (an MMA of N = 64 takes 48 cycles, not 32: 302 us
 // against 284 at the time); two threads a row on 16 warps (284 against 275); an
 // eighth to a half of the exponentials as polynomials on the FMA pipe (235 to 280
-// us); the halves' exponentials taking turns (287 against 266).
+// us); the halves' exponentials taking turns (287 against 266); the next
+// segment's queries fetched before a segment's outputs are written (spills: 247
+// us against 216).
 // Tensor memory: S_h (128 columns, P over the last 64), O_0 O_1 (D each).
 // Shared memory: Q 2 x 128 x D, two stages of K and of V (128 x D each), fp16.
 //
