@@ -216,8 +216,8 @@ def kv4_attention(q: torch.Tensor, cache, kv_len: torch.Tensor, block_table: tor
     Request b has kv_len[b] keys (int32, the new tokens' own among them), key j in page block_table[b, j //
     page_size] (int32, (requests, max_pages)); its queries are tokens q_start[b] .. q_start[b + 1] (int32,
     (requests + 1,), ascending; None: the same number each) and stand at its last positions.  causal: a query
-    sees keys up to its own position, else all.  out may not overlap q.  softmax_scale defaults to 1 / sqrt(head_dim).  max_kv_len, an
-    upper bound of kv_len known to the caller, only steers how the work is split.
+    sees keys up to its own position, else all.  softmax_scale defaults to 1 / sqrt(head_dim).  max_kv_len, an
+    upper bound of kv_len known to the caller, only steers how the work is split.  out may not overlap q.
 
     Returns out (tokens, q_heads, head_dim), with ``return_lse`` also the log sums (tokens, q_heads) fp32.  A
     query without keys gets 0 and -inf.  Tokens of no request are left as they were (in a new output:

@@ -339,7 +339,10 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.block_table = static_cast<const int*>(table.data_ptr());
     d.table_stride = table.stride(0);
     d.max_pages = count(table.size(1), "block_table");
-    if (given(a[4])) d.q_start = static_cast<const int*>(vector(a[4], "q_start", at::kInt, (int64_t)d.requests + 1, &device).data_ptr());
+    if (given(a[4])) {
+      const at::Tensor& start = vector(a[4], "q_start", at::kInt, (int64_t)d.requests + 1, &device);
+      d.q_start = static_cast<const int*>(start.data_ptr());
+    }
     d.causal = truth(a[5]);
     d.softmax_scale = (float)(given(a[6]) ? number(a[6]) : 1.0 / std::sqrt((double)d.cache.head_dim));
     if (given(a[7])) {

@@ -744,7 +744,8 @@ cudaError_t launch_join(const Kv4AttnLaunch& p, cudaStream_t stream) {
                         32 * kWarpsJ, 0, stream, p);
   if (p.tile_rows > 32) {
     const int items = (p.ctas - 1) * (p.tile_rows / kRowsJ);
-    return launch_after(kv4_join_rows_kernel<D, BF16>, dim3((unsigned)(items + kWarpsJ - 1) / kWarpsJ), 32 * kWarpsJ, 0, stream, p);
+    return launch_after(kv4_join_rows_kernel<D, BF16>, dim3((unsigned)(items + kWarpsJ - 1) / kWarpsJ), 32 * kWarpsJ, 0,
+                        stream, p);
   }
   const long long blocks = ((long long)(p.ctas - 1) * p.tile_rows + kWarpsJ - 1) / kWarpsJ, most = 16ll * p.num_sms;
   return launch_after(kv4_join_kernel<D, 1, BF16>, dim3((unsigned)(blocks < most ? blocks : most)), 32 * kWarpsJ, 0, stream, p);
