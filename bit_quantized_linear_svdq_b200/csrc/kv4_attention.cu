@@ -40,7 +40,7 @@
 // 128, up to 8 rows) at 3.2 a clock, of which 256 convert and scale the 8192
 // values (cvt.e2m1x2 takes any byte of a register; the same from shifts and
 // logic is 2.2 times slower).  64 sequences of up to 8192 keys, 32 query and 8
-// key heads: 103 us, 4.4 TB/s; two of 131059 keys, 4 key heads: 40 us, 3.7 TB/s;
+// key heads: 102 us, 4.4 TB/s; two of 131059 keys, 4 key heads: 40 us, 3.7 TB/s;
 // one of 1021 keys: 8.0 us, set-up and latencies.  16-key tiles: 128 us on the
 // first; five CTAs an SM, with spills, 129.
 //
@@ -518,10 +518,10 @@ __global__ void __launch_bounds__(kThreadsA, ctas_per_sm(D, NT))
 
 // Joins the parts of segments that several CTAs took, row by row: item (c, r)
 // is row r of the segment that CTA c began and did not finish (the first kernel
-// left a note of it).  WR warps take an item: 1, while a segment has a few
-// parts, or all 8, and then a CTA looks at 32 notes at once for the few that
-// exist.  Warp w of them adds parts w, w + WR, ..., eight in flight, and the
-// warps' sums are added in order.
+// left a note of it).  WR warps take an item: 1, while a segment has five to
+// eight parts (fewer: the kernel below), or all 8, and then a CTA looks at 32
+// notes at once for the few that exist.  Warp w of them adds parts w, w + WR,
+// ..., eight in flight, and the warps' sums are added in order.
 constexpr int kWarpsJ = 8;
 template <int D, int WR, bool BF16>
 __global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_kernel(const __grid_constant__ Kv4AttnLaunch p) {
@@ -630,10 +630,11 @@ __global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_kernel(const __grid_con
   }
 }
 
-// The same for tiles of 256 rows, mostly in two or three parts: a warp takes two
-// rows of a note, two parts of each in flight.  After the prompt chunks that
+// The same where a segment has a few parts at most: a warp takes two rows of a
+// note, two parts of each in flight.  After the prompt chunks that
 // kv4_attention_tc.cu measures (147 notes, about 40 MB of parts) this takes 12
-// us, the kernel above 28, four rows a warp 17, one 14.
+// us, the kernel above 28, four rows a warp 17, one 14; after 16 requests of 32
+// rows and 4096 keys 2 us less than the one above, of 64 rows 4.
 constexpr int kRowsJ = 2;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_rows_kernel(const __grid_constant__ Kv4AttnLaunch p) {
@@ -714,9 +715,9 @@ __global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_rows_kernel(const __gri
 // Requests of at most kFewRows rows (query heads of one key head x tokens) go to
 // this file's kernel, larger ones to kv4_attention_tc.cu.  Both measured, us at
 // 32 / 64 / 96 / 128 rows a request, 8 key heads, D = 128: one request of 4096
-// keys 14.8 / 19.6 / 28.3 / 27.5 here, 20.4 / 20.6 / 21.0 / 23.6 there; 16 of
-// them 53 / 86 / 124 / 153 and 79 / 81 / 83 / 86 (D = 64: 35 / 57 / 79 / 98 and
-// 63 / 64 / 66 / 68).
+// keys 14.9 / 19.6 / 28.9 / 27.7 here, 20.6 / 20.6 / 21.1 / 23.9 there; 16 of
+// them 51 / 82 / 119 / 149 and 72 / 73 / 75 / 77 (D = 64: 34 / 54 / 76 / 95 and
+// 59 / 60 / 60 / 61).
 constexpr int kFewRows = 64, kFewRowsInAll = 512;
 
 size_t parts_bytes(const Kv4AttnLaunch& p) {
@@ -742,7 +743,7 @@ cudaError_t launch_join(const Kv4AttnLaunch& p, cudaStream_t stream) {
   if (p.ctas > 8 * p.segments)
     return launch_after(kv4_join_kernel<D, kWarpsJ, BF16>, dim3((unsigned)(p.ctas + 31) / 32, (unsigned)p.tile_rows),
                         32 * kWarpsJ, 0, stream, p);
-  if (p.tile_rows > 32) {
+  if (p.ctas <= 4 * p.segments) {
     const int items = (p.ctas - 1) * (p.tile_rows / kRowsJ);
     return launch_after(kv4_join_rows_kernel<D, BF16>, dim3((unsigned)(items + kWarpsJ - 1) / kWarpsJ), 32 * kWarpsJ, 0,
                         stream, p);

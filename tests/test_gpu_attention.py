@@ -406,6 +406,9 @@ ATTEND = [
     ([900, 31, 400, 65], [0, 200, 201, 401, 402], 6, 2, 128, 32, True, BF),   # prompts beside single tokens
     ([900, 31, 400, 65], [3, 300, 301, 310, 311], 4, 2, 64, 16, False, FP),
     ([260, 0, 129], [0, 129, 400, 700], 2, 1, 128, 16, True, FP),  # a prompt without keys; more queries than keys
+    ([300, 450, 40], 1, 7, 1, 128, 16, True, BF),                  # two to four parts a segment, an odd number of rows
+    ([400, 300], 33, 15, 5, 128, 64, True, FP),
+    ([511, 260], 41, 9, 3, 64, 32, False, BF),
 ]
 
 
