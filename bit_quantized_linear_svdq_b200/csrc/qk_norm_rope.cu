@@ -31,10 +31,10 @@
 //
 // Bound: 4 bytes an element (HBM).  4096 tokens x 64 heads x 128, norms and
 // adjacent pairs: 25.4 us, 5.3 TB/s (the loads and stores alone 23.9).  The
-// Hadamard is bound by the shared-memory pipe instead, 128 bytes a clock: per
-// four rows of 128, 51 wavefronts of shuffles, 32 of cosines, sines and weights
-// and 16 of loads and stores: 9973 tokens x 32 heads 43.9 us, 3.7 TB/s (with
-// bank conflicts on the tables 48.7).  29991 tokens x 40 heads x 64, 48 values
+// Hadamard is bound by instruction issue (about 400 per four rows of 128, 70% of
+// the slots) and the shared-memory pipe (51 wavefronts of shuffles, 32 of
+// cosines, sines and weights, 16 of loads and stores, 66%) instead: 9973 tokens x
+// 32 heads 43.9 us, 3.7 TB/s (with bank conflicts on the tables 48.7).  29991 tokens x 40 heads x 64, 48 values
 // of a head rotated: 58.0 us, 5.3 TB/s.  Three or five CTAs an SM instead of
 // four: 29.2 / 46.4 / 64.8 and 30.8 / 50.2 / 66.1 us.  One kernel for every
 // pairing, with and without the Hadamard, instead of six: 27.9 / 48.7 / 64.1.
