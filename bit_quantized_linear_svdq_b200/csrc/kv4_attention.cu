@@ -717,8 +717,8 @@ __global__ void __launch_bounds__(32 * kWarpsJ) kv4_join_rows_kernel(const __gri
 // 32 / 64 / 96 / 128 rows a request, 8 key heads, D = 128: one request of 4096
 // keys 14.9 / 19.6 / 28.9 / 27.7 here, 20.6 / 20.6 / 21.1 / 23.9 there; 16 of
 // them 51 / 82 / 119 / 149 and 72 / 73 / 75 / 77 (D = 64: 34 / 54 / 76 / 95 and
-// 59 / 60 / 60 / 61).
-constexpr int kFewRows = 64, kFewRowsInAll = 512;
+// 59 / 60 / 60 / 61).  Where the sizes are on the device split_rows (kv4_rows.cuh)
+// goes by their sum.
 
 size_t parts_bytes(const Kv4AttnLaunch& p) {
   return p.join ? (size_t)p.ctas * (2 * p.tile_rows * ((size_t)p.c.D * 4 + 8) + sizeof(Kv4Cut)) : 0;
@@ -791,18 +791,9 @@ Kv4Plan kv4_attention_plan(const Kv4AttnLaunch& base, int max_kv, int num_sms) {
   plan.few = plan.many = base;
   plan.few.num_sms = plan.many.num_sms = num_sms;
   const long long rows = (long long)base.tokens * (base.q_heads / base.c.heads);
-  constexpr int kAll = 0x7FFFFFFF;
-  if (!base.q_start) {
-    plan.use_many = rows > (long long)kFewRows * base.requests;
-    plan.use_few = !plan.use_many;
-  } else {
-    // The requests' sizes are on the device: each kernel takes its own.  A few
-    // hundred rows in all are left to the one kernel, and where requests have
-    // 256 rows on average all of them to the other: small requests among them
-    // take no more of its tiles than the large ones.
-    plan.use_many = rows > kFewRowsInAll;
-    plan.use_few = rows < 256ll * base.requests;
-  }
+  const RowSplit split = split_rows(rows, base.requests, base.q_start != nullptr);
+  plan.use_few = split.few;
+  plan.use_many = split.many;
   // The smallest tile that holds an average request's rows: a larger one
   // dequantizes each key for more rows at once, a smaller one leaves room for
   // more warps (20 rows, 16 x 3001 keys, 8 heads: tiles of 24 rows 35.1 us, of
@@ -811,8 +802,8 @@ Kv4Plan kv4_attention_plan(const Kv4AttnLaunch& base, int max_kv, int num_sms) {
   long long each = base.requests > 0 ? (rows + base.requests - 1) / base.requests : 0;
   if (base.q_start && plan.use_many) each = base.q_heads / base.c.heads;
   const int nt = each <= 8 ? 1 : each <= 16 ? 2 : each <= 24 ? 3 : 4;
-  plan_launch(plan.few, 8 * nt, 0, plan.use_many ? kFewRows : kAll, (long long)num_sms * ctas_per_sm(base.c.D, nt), max_kv);
-  plan_launch(plan.many, 256, plan.use_few ? kFewRows + 1 : 0, kAll, num_sms, max_kv);
+  plan_launch(plan.few, 8 * nt, 0, split.few_max, (long long)num_sms * ctas_per_sm(base.c.D, nt), max_kv);
+  plan_launch(plan.many, 256, split.many_min, 0x7FFFFFFF, num_sms, max_kv);
   return plan;
 }
 

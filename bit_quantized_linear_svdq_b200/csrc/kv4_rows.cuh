@@ -163,6 +163,32 @@ KV4_HD long long max_units(int tokens, int requests, int group, int heads, int t
   return tiles * heads * tile_units(max_kv);
 }
 
+// Which requests of a call each kernel takes, by their rows (query heads of one
+// key head x tokens).  Every size that the call can hold belongs to one of the
+// two that are launched (tests/native/kv4_plan_check.cpp).
+struct RowSplit {
+  bool few, many;                               // launched
+  int few_max, many_min;                        // rows of a request at most / at least
+};
+constexpr int kFewRows = 64, kFewRowsInAll = 512, kManyRowsEach = 256;
+KV4_HD RowSplit split_rows(long long rows, int requests, bool ragged) {
+  RowSplit s;
+  if (!ragged) {                                // the requests are alike
+    s.many = rows > (long long)kFewRows * requests;
+    s.few = !s.many;
+  } else {
+    // The requests' sizes are on the device: each kernel takes its own.  Where
+    // requests have 256 rows on average all of them go to the many-row kernel:
+    // small requests among them take no more of its tiles than the large ones.
+    // Fewer are left to the few-row kernel up to a few hundred rows in all.
+    s.few = rows < (long long)kManyRowsEach * requests;
+    s.many = !s.few || rows > kFewRowsInAll;
+  }
+  s.few_max = s.many ? kFewRows : 0x7FFFFFFF;
+  s.many_min = s.few ? kFewRows + 1 : 0;
+  return s;
+}
+
 #if defined(__CUDACC__)
 // Warp-wide view of the launch's units: total, and the first unit of a request.
 // Every lane calls with the same arguments.

@@ -197,3 +197,26 @@ def test_rope_frequencies():
     for bad in ((), (-1,), (1.5,)):
         with pytest.raises(ValueError):
             S.rope_frequencies(bad, device="cpu")
+
+
+# ------------------------------------------------------------------ which kernel takes a request
+
+def test_every_size_of_a_call_belongs_to_one_kernel(tmp_path):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    exe = str(tmp_path / "kv4_plan_check")
+    subprocess.run([cxx, "-O2", "-std=c++17", "-I", B.CSRC, os.path.join(ROOT, "tests", "native", "kv4_plan_check.cpp"),
+                    "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout
+    assert r.stdout.strip() == "ok"
+
+
+@pytest.mark.parametrize("requests", [1, 2, 3, 40])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_every_size_of_a_call_is_planned(lib, requests, ragged):
+    """Over a long table each launch shares its segments among CTAs, so a call that launches anything needs a workspace."""
+    for tokens in range(requests, 1100, 1 if requests == 1 else requests):
+        d = _attn(tokens=tokens, requests=requests, max_pages=4096, q_start=256 if ragged else None)
+        assert lib.svdq_kv4_attention_workspace_bytes(ctypes.addressof(d)) > 0, tokens

@@ -731,3 +731,18 @@ def test_attention_block_from_projection_to_projection(rotate):
     torch.cuda.synchronize()
     assert layer.device_status() == 0
     layer.close()
+
+
+# ------------------------------------------------------------------ every size of a ragged call reaches a kernel
+
+@pytest.mark.parametrize("start,group,dim", [([0, r], 1, 64) for r in (64, 65, 255, 256, 257, 511, 512, 513)] +
+                         [([0, 64], 4, 128), ([0, 75], 4, 128), ([0, 128], 4, 128), ([0, 100, 512], 1, 128),
+                          ([0, 256, 512], 1, 64), ([0, 1, 512], 1, 64), ([0, 0, 511, 512], 1, 64), ([130, 150], 2, 128)])
+def test_ragged_calls_of_any_size_are_answered(start, group, dim):
+    """(check fills the output with another value first; [130, 150] is one request in the middle of a padded batch.)"""
+    n = len(start) - 1
+    case = ([690, 300, 61][:n], start, group, 1, dim, 32, True, BF)
+    q, cache, lens, table, start, causal = make(case, 101)
+    q = q[:-1] if start[0] == 0 else torch.cat((q, q))          # as many rows as the requests have; or rows behind them
+    check(q, cache, lens, table, start, causal)
+    check(q, cache, lens, table, start, False, max_kv_len=max(lens))
