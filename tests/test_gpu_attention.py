@@ -746,3 +746,46 @@ def test_ragged_calls_of_any_size_are_answered(start, group, dim):
     q = q[:-1] if start[0] == 0 else torch.cat((q, q))          # as many rows as the requests have; or rows behind them
     check(q, cache, lens, table, start, causal)
     check(q, cache, lens, table, start, False, max_kv_len=max(lens))
+
+
+# ------------------------------------------------------------------ the ends of the softmax scale and of the queries
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-30, -1e-40])
+@pytest.mark.parametrize("case", ATTEND, ids=lambda c: f"{c[0]}-{c[1]}-{c[2:7]}".replace(" ", ""))
+def test_scales_of_zero_and_next_to_it(case, scale):
+    """All keys that a query sees weigh alike; masked ones nothing."""
+    q, cache, lens, table, start, causal = make(case, 111)
+    check(q, cache, lens, table, start, causal, scale=scale)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_tiny_queries_and_scales_of_many_rows(causal):
+    """The factor of a row's exponents falls below fp32's range; rows without keys among them."""
+    case = ([100, 70, 0], [0, 120, 190, 260], 2, 1, 128, 16, causal, BF)
+    q, cache, lens, table, start, _ = make(case, 112)
+    check(q * 1e-37, cache, lens, table, start, causal, scale=1e-5)
+    check(q * 1e-37, cache, lens, table, start, causal)
+    check(torch.zeros_like(q), cache, lens, table, start, causal)
+    table[0, 1] = -1                                             # 16 keys in no page
+    check(q, cache, lens, table, start, causal, scale=0.0)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, FP), (128, BF)])
+@pytest.mark.parametrize("new", [4, 150])
+def test_special_queries_of_few_and_many_rows(new, dim, dtype):
+    case = ([200], new, 2, 1, dim, 16, True, dtype)
+    q, cache, lens, table, start, causal = make(case, 113)
+    lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for scale in (None, 0.0):
+        clean = S.kv4_attention(q, cache, lens_t, table, softmax_scale=scale).float()
+        x = q.clone()
+        x[1, 0, 3], x[new - 1, 1, 4], x[new // 2, 1] = float("nan"), float("inf"), float("-inf")
+        got = S.kv4_attention(x, cache, lens_t, table, softmax_scale=scale).float()
+        bad = torch.zeros(new, 2, dtype=torch.bool)
+        bad[1, 0] = bad[new - 1, 1] = bad[new // 2, 1] = True
+        assert got[bad].isnan().all() and torch.equal(got[~bad], clean[~bad])
+    # The type's ends: tiny queries weigh all keys alike, the largest ones are scaled back into range.
+    big = torch.finfo(dtype).max
+    tiny = torch.finfo(dtype).tiny
+    check(torch.full_like(q, tiny), cache, lens, table, None, True)
+    check((torch.sign(q) * big).to(dtype), cache, lens, table, None, True, scale=0.5 / big)
