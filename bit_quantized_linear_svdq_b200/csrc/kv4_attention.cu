@@ -20,8 +20,9 @@
 // fp16, so dequantizing (cvt.e2m1x2, one packed multiply) rounds nothing.
 // Queries are scaled per row by a power of two into fp16's range: bf16's 8 bits
 // fit, and what falls below fp16's smallest subnormal is under 2^-38 of the
-// row's largest value.  The softmax (base 2) is fp32; its weights, in [0, 1], are
-// rounded to fp16 (2^-11 relative) for the second product only.
+// row's largest value.  The softmax (base 2) is fp32; its weights are rounded to
+// fp16 for the second product only: 2^-11 relative, or 2^-32 of the row's largest
+// (kv4_common.cuh).
 //
 // Layout.  Both products are transposed, keys (dims) on the MMA's 16 rows and
 // query rows on its 8 columns: at one to eight query rows a key head, the usual
@@ -287,7 +288,7 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
     }
 
     // ---- weights.  s[u][.][0..1]: key kg + 16u, rows 2t and 2t + 1; s[u][.][2..3]: key kg + 16u + 8.  The reference
-    // exponent is raised only when a score exceeds it by more than 2^8 (or at a row's first key): weights stay below 2^8.
+    // exponent is raised only when a score exceeds it by more than kMost (or at a row's first key).
     const bool masked = gone != 0 || k0 + kTileA > free_end;
     const int kg = k0 + (g >> 1) + 4 * (g & 1);
     float x[2][NT][4];
@@ -318,7 +319,7 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
 #pragma unroll
       for (int c = 0; c < 2; ++c)
         over |= fmaxf(fmaxf(x[0][n][c], x[0][n][2 + c]), fmaxf(x[1][n][c], x[1][n][2 + c])) >
-                (ref[n][c] == -INFINITY ? -INFINITY : 8.0f);
+                (ref[n][c] == -INFINITY ? -INFINITY : kMost);
     if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -328,7 +329,7 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
           v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
           v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
-          const float to = ref[n][c] == -INFINITY ? v : ref[n][c] + fmaxf(v, 0.0f);
+          const float to = ref[n][c] == -INFINITY ? v - kRoom : ref[n][c] + fmaxf(v - kRoom, 0.0f);
           const float f = ex2_diff(ref[n][c], to);
           ref[n][c] = to;
           sum[n][c] *= f;

@@ -18,7 +18,7 @@
 //                    (with 152 registers and half of them read twice: 266 us
 //                    against 231 at the time), weights go back there as fp16
 //                    over the scores; the output is rescaled there only when
-//                    the reference exponent rises by more than 8.
+//                    the reference exponent has to rise (by more than 8).
 //   warps 8-11       thread = key of the tile: 4-bit rows -> fp16 rows in shared
 //                    memory, K and V in the same layout (128-byte swizzled rows
 //                    of 64 dims): K is the first product's K-major operand, V
@@ -40,7 +40,8 @@
 //
 // Numerics are those of kv4_attention.cu: cache values exact in fp16, queries
 // scaled per row by a power of two (and the sign of the softmax scale), fp32
-// sums, weights rounded to fp16 for the second product.  A NaN value in a tile
+// sums, weights rounded to fp16 for the second product (2^-11, or 2^-32 of the
+// row's largest).  A NaN value in a tile
 // that some rows see only in part is written as zero and remembered per row.
 //
 // Every wait is bounded; one that runs out sets an error word
@@ -374,11 +375,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
           for (int i = 0; i < 32; i += 2)
             tops[c] = max3(tops[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
         const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
-        // Relative to the reference (the first key's own, then raised past 2^8 only).
+        // Relative to the reference (kRoom below the first tile's largest, then raised past kMost only).
         const float rel = ref == -INFINITY ? top * qs : fmaf(top, qs, -ref);
-        const bool over = ref == -INFINITY ? top > -INFINITY : rel > 8.0f;
+        const bool over = ref == -INFINITY ? top > -INFINITY : rel > kMost;
         if (__any_sync(0xFFFFFFFFu, over)) {
-          const float to = over ? (ref == -INFINITY ? rel : ref + rel) : ref;
+          const float to = over ? (ref == -INFINITY ? rel : ref + rel) - kRoom : ref;
           const float f = over ? ex2_diff(ref, to) : 1.0f;
           ref = to;
           sum *= f;
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
           p.part_ml[part_row + row] = make_float2(ref, sum);
         else if (p.lse)
           p.lse[(long long)(job.rt.token0 + tok) * p.q_heads + head] =
-              sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+              sum == 0.0f ? -INFINITY : log_sum(ref, sum);
       }
       tc_fence_before_sync();
     }

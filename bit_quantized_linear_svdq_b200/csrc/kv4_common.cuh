@@ -13,6 +13,12 @@
 namespace svdq {
 
 constexpr float kLog2e = 1.4426950408889634f;
+// Weights are 2^(score - ref), rounded to fp16 for the product with the values.
+// A row's reference is first set kRoom below its largest score, so that weights
+// begin at 2^7, and set again when one would pass 2^kMost, half of fp16's range:
+// what is lost below fp16's range is 2^-32 of the largest weight, not 2^-25 (over
+// 131072 keys 2^-15 of a value at most, not 2^-8).
+constexpr float kRoom = 7.0f, kMost = 15.0f;        // (log_sum has 2^-kRoom as a number)
 constexpr uint32_t kAbsent = 0xFFFFFFFFu;             // no such cache row: past the keys, or in no page of the cache
 
 __device__ __forceinline__ uint32_t hmul2u(uint32_t a, __half2 b) {
@@ -53,6 +59,12 @@ __device__ __forceinline__ int row_exponent(float big) {
   return big > 0.0f ? min(max(14 - (int)((__float_as_uint(big) >> 23) & 0xFF) + 127, -126), 126) : 0;
 }
 
+// A row's log sum from its reference and its sum of weights (not 0).  The room is taken out of both first: a log of
+// about 7 next to a reference of about -7 would round coarser than their sum.
+__device__ __forceinline__ float log_sum(float ref, float total) {
+  return (ref + kRoom + log2f(total * 0x1p-7f)) * 0.6931471805599453f;
+}
+
 // One 8-element piece of an output row: v / total in the storage type, and the
 // row's log sum.  total == 0: the row saw no key (or only scores of -inf).
 template <bool BF16>
@@ -66,7 +78,7 @@ __device__ __forceinline__ void store_row8(const Kv4AttnLaunch& p, long long tok
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + token * p.ot + head * p.oh + d0) =
       make_uint4(w[0], w[1], w[2], w[3]);
   if (p.lse && d0 == 0)
-    p.lse[token * p.q_heads + head] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
+    p.lse[token * p.q_heads + head] = total == 0.0f ? -INFINITY : log_sum(top, total);
 }
 
 __device__ __forceinline__ Kv4Work work_of(const Kv4AttnLaunch& p) {

@@ -111,7 +111,8 @@ SVDQ_API svdq_status svdq_kv4_read(const svdq_kv4_cache* cache, const svdq_heads
  * as they were in out and lse.  Lengths are clamped to the table's capacity;
  * keys in a page outside [0, pages) do not exist.  q_start has to ascend.
  * q and out must not overlap.  Products are exact in fp32 per term, sums and
- * softmax fp32, softmax weights rounded to fp16 for the product with v.
+ * softmax fp32, softmax weights rounded to fp16 for the product with v (2^-11
+ * of themselves, or 2^-32 of the row's largest where that is more).
  * max_kv_len: an upper bound of kv_len for scheduling (0: the table's
  * capacity); a too small one costs time, not correctness.
  * workspace: svdq_kv4_attention_workspace_bytes(desc) bytes, 16-byte aligned,

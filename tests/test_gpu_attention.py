@@ -789,3 +789,38 @@ def test_special_queries_of_few_and_many_rows(new, dim, dtype):
     tiny = torch.finfo(dtype).tiny
     check(torch.full_like(q, tiny), cache, lens, table, None, True)
     check((torch.sign(q) * big).to(dtype), cache, lens, table, None, True, scale=0.5 / big)
+
+
+# ------------------------------------------------------------------ many small weights beside a large one
+
+@pytest.mark.parametrize("new,dim,dtype", [(1, 128, BF), (1, 64, FP), (20, 128, FP), (80, 128, BF), (80, 64, FP), (300, 64, BF)])
+def test_many_small_weights_beside_a_large_one(new, dim, dtype):
+    """Every 32nd key weighs 2^26 times the others and has values of zero: the output is what the others leave.  The
+    bound is attend_reference's with the weights' absolute rounding where it has to lie: a weight is rounded to fp16
+    after a factor of at least 2^7, so to 2^-25 / 2^7 of the largest one (below fp16's normal range), and to 2^-11 of
+    itself above it; the sum of weights divides both."""
+    keys, page = 3000, 64
+    pages = -(-keys // page)
+    cache = S.kv4_cache(pages, page, 1, dim)
+    n = pages * page
+    large = torch.arange(n, device="cuda") % 32 == 0
+    k = torch.zeros(n, 1, dim, dtype=dtype, device="cuda")
+    k[:, 0, 0] = torch.where(large, 6.0, -6.0).to(dtype)
+    v = torch.rand(n, 1, dim, device="cuda", generator=gen(121)) + 0.5
+    v[large] = 0
+    S.kv4_append(cache, k, v.to(dtype), torch.arange(n, device="cuda"))
+    q = torch.zeros(new, 1, dim, dtype=dtype, device="cuda")
+    q[..., 0] = 1
+    scale = float(np.float32(26 * math.log(2) / 12))
+    table = torch.arange(pages, device="cuda", dtype=torch.int32)[None]
+    out, lse = S.kv4_attention(q, cache, torch.tensor([keys], dtype=torch.int32, device="cuda"), table, causal=False,
+                               softmax_scale=scale, return_lse=True)
+    kk, vv = (values(cache, i).reshape(n, dim)[:keys] for i in (0, 2))
+    s = kk[:, 0] * scale
+    l = torch.logsumexp(s, 0)
+    want = torch.exp(s - l) @ vv
+    ds = 2.0 ** -23 * (dim + 4) * 6 * scale + 2.0 ** -22 * (6 * scale + 1)
+    bound = (2.0 ** -11 + 2 * ds + 2 * keys * 2.0 ** -24) * want + 2.0 ** -32 * vv.sum(0) / torch.exp(l - s.max())
+    assert (bound < 0.02 * want).all()                          # (a bound that would notice their absence)
+    assert_rounded(out[:, 0], want.expand(new, dim), bound.expand(new, dim), dtype)
+    assert ((lse.double() - l).abs() <= ds + keys * 2.0 ** -24 + 2.0 ** -22 * (1 + l.abs())).all()
