@@ -164,7 +164,7 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, q_weight: Op
     q (tokens, q_heads, head_dim), k (tokens, k_heads, head_dim) or None; weights (head_dim,); positions
     (tokens,) or (tokens, axes) int32; inv_freq (pairs,) fp32; pair_axis (pairs,) uint8, the axis of each pair
     (None: axis 0); pairs are adjacent channels if ``interleaved``, else channels p and p + pairs.  Returns
-    (q, k), new and contiguous, or the arguments themselves, written over, if ``inplace``.
+    (q, k), new and contiguous, or the arguments themselves, written over, if ``inplace`` (q and k may not overlap then).
     """
     return _run((_native or _calls()).qk_norm_rope, "svdq_qk_norm_rope", q, stream, q, k, q_weight, k_weight, eps, positions,
                 inv_freq, pair_axis, interleaved, hadamard, inplace)
@@ -195,7 +195,8 @@ def kv4_cache(pages: int, page_size: int, heads: int, head_dim: int, device="cud
 
 def kv4_append(cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
     """Quantize k, v (tokens, heads, head_dim) into the cache: token t goes to slot ``slots[t]`` = page *
-    page_size + offset (int64).  Slots outside the cache (-1 for padding) are skipped; the others must differ."""
+    page_size + offset (int64).  Slots outside the cache (-1 for padding) are skipped; the others must differ.  The
+    cache's four tensors, k, v and slots may share a buffer, but not memory."""
     _run((_native or _calls()).kv4_append, "svdq_kv4_append", k, stream, cache, k, v, slots)
 
 
@@ -217,7 +218,7 @@ def kv4_attention(q: torch.Tensor, cache, kv_len: torch.Tensor, block_table: tor
     page_size] (int32, (requests, max_pages)); its queries are tokens q_start[b] .. q_start[b + 1] (int32,
     (requests + 1,), ascending; None: the same number each) and stand at its last positions.  causal: a query
     sees keys up to its own position, else all.  softmax_scale defaults to 1 / sqrt(head_dim).  max_kv_len, an
-    upper bound of kv_len known to the caller, only steers how the work is split.  out may not overlap q.
+    upper bound of kv_len known to the caller, only steers how the work is split.  out may not overlap any argument.
 
     Returns out (tokens, q_heads, head_dim), with ``return_lse`` also the log sums (tokens, q_heads) fp32.  A
     query without keys gets 0 and -inf.  Tokens of no request are left as they were (in a new output:

@@ -12,13 +12,13 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
-#include <ATen/MemoryOverlap.h>
 
 #include <cmath>
 #include <cstdarg>
 #include <string>
 #include <utility>
 
+#include "head_overlap.h"
 #include "svdq_attn.h"
 
 namespace {
@@ -106,12 +106,27 @@ void distinct(const at::Tensor& t, const char* name) {
     extent += t.stride(i) * (t.size(i) - 1);
   }
 }
+// The memory of an argument: a tensor of heads, a block table (rows of contiguous numbers), or a contiguous tensor.
+struct Memory {
+  svdq::HeadRuns runs;                          // bytes 0: none
+  const char* name;
+  Memory() = default;
+  Memory(const at::Tensor& t, const char* n) : name(n) {
+    const long long size = (long long)t.element_size(), at = (long long)reinterpret_cast<uintptr_t>(t.data_ptr());
+    if (t.numel() == 0)
+      runs = {at, 0, 0, 1, 1, 0};
+    else if (t.dim() == 3)
+      runs = {at, t.stride(0) * size, t.stride(1) * size, t.size(0), t.size(1), t.size(2) * size};
+    else if (t.dim() == 2)
+      runs = {at, t.stride(0) * size, 0, t.size(0), 1, t.size(1) * size};
+    else
+      runs = {at, 0, 0, 1, 1, (long long)t.numel() * size};
+  }
+};
 // Refuses an output that lies over another argument (views of one buffer side by side are fine).
-void apart(const at::Tensor& t, const char* name, const at::Tensor& other, const char* other_name) {
-  if (t.numel() == 0 || other.numel() == 0 || !t.is_alias_of(other)) return;
-  const auto status = at::get_overlap_status(t, other);
-  if (status == at::MemOverlapStatus::Full || status == at::MemOverlapStatus::Partial || t.data_ptr() == other.data_ptr())
-    raise(PyExc_ValueError, "%s and %s overlap in memory", name, other_name);
+void apart(const Memory& t, const Memory& other) {
+  if (t.runs.bytes == 0 || other.runs.bytes == 0 || !svdq::runs_overlap(t.runs, other.runs)) return;
+  raise(PyExc_ValueError, "%s and %s overlap in memory", t.name, other.name);
 }
 // A contiguous vector of n elements (n < 0: any number).
 const at::Tensor& vector(PyObject* o, const char* name, at::ScalarType type, int64_t n, int* device) {
@@ -123,7 +138,8 @@ const at::Tensor& vector(PyObject* o, const char* name, at::ScalarType type, int
   return t;
 }
 
-svdq_kv4_cache cache_of(PyObject* o, int* device) {
+// `memory`: that of the four, if wanted.
+svdq_kv4_cache cache_of(PyObject* o, int* device, Memory* memory = nullptr) {
   static const char* names[4] = {"k_codes", "k_scales", "v_codes", "v_scales"};
   PyObject* seq = PySequence_Fast(o, "cache: expected (k_codes, k_scales, v_codes, v_scales)");
   if (!seq) throw PythonError();
@@ -155,6 +171,7 @@ svdq_kv4_cache cache_of(PyObject* o, int* device) {
             c.head_dim / (scales ? 16 : 2), shape_text(t).c_str());
     if (!t.is_contiguous()) raise(PyExc_ValueError, "%s: must be contiguous", names[i]);
     data[i] = t.data_ptr();
+    if (memory) memory[i] = Memory(t, names[i]);
   }
   c.k_codes = data[0];
   c.k_scales = data[1];
@@ -259,7 +276,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       distinct(q, "q");
       if (k) {
         distinct(*k, "k");
-        apart(q, "q", *k, "k");
+        apart(Memory(q, "q"), Memory(*k, "k"));
       }
       d.q_out = d.q;
       d.k_out = d.k;
@@ -283,13 +300,19 @@ PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int device = -1;
     const at::Tensor& k = on_device(a[1], "k", &device);
     const int dtype = type_code(k, "k");
-    const svdq_kv4_cache c = cache_of(a[0], &device);
+    Memory cache[4];
+    const svdq_kv4_cache c = cache_of(a[0], &device, cache);
     const at::Tensor& slots = vector(a[3], "slots", at::kLong, -1, &device);
     const at::Tensor& v = on_device(a[2], "v", &device);
     need_type(v, "v", k.scalar_type());
     need_shape(k, "k", slots.size(0), c.heads, c.head_dim);
     need_shape(v, "v", slots.size(0), c.heads, c.head_dim);
     const svdq_heads ka = heads_of(k, "k"), va = heads_of(v, "v");
+    const Memory inputs[3] = {Memory(k, "k"), Memory(v, "v"), Memory(slots, "slots")};
+    for (int i = 0; i < 4; ++i) {
+      for (const Memory& m : inputs) apart(cache[i], m);
+      for (int j = 0; j < i; ++j) apart(cache[i], cache[j]);
+    }
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
     return answer(svdq_kv4_append(&c, &ka, &va, count(slots.size(0), "slots"), dtype,
                                   static_cast<const long long*>(slots.data_ptr()), current_stream(device)),
@@ -321,7 +344,8 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     svdq_kv4_attention_desc d = {};
     const at::Tensor& q = on_device(a[0], "q", &device);
     d.dtype = type_code(q, "q");
-    d.cache = cache_of(a[1], &device);
+    Memory cache[4];
+    d.cache = cache_of(a[1], &device, cache);
     d.q = heads_of(q, "q");
     d.tokens = count(q.size(0), "q");
     d.q_heads = count(q.size(1), "q");
@@ -358,7 +382,12 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       need_shape(out, "out", q.size(0), q.size(1), q.size(2));
       d.out = heads_of(out, "out");
       distinct(out, "out");
-      apart(out, "out", q, "q");
+      const Memory written(out, "out");
+      apart(written, Memory(q, "q"));
+      for (const Memory& m : cache) apart(written, m);
+      apart(written, Memory(lens, "kv_len"));
+      apart(written, Memory(table, "block_table"));
+      if (given(a[4])) apart(written, Memory(tensor(a[4], "q_start"), "q_start"));
     } else {
       out = empty(q.sizes(), q, q.scalar_type());
       d.out = contiguous_heads(out);

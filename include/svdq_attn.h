@@ -82,7 +82,9 @@ typedef struct {
  * svdq_kv4_append -- quantize k, v (tokens, heads, head_dim) into the cache:
  * token t goes to slot slots[t] = page * page_size + offset (int64, device).
  * A slot outside the cache (negative: padding) is skipped.  The slots of one
- * call have to differ; a slot named twice is left with an unspecified mix.
+ * call have to differ; a slot named twice is left with an unspecified mix.  The
+ * cache's tensors may not overlap each other, k, v or slots here (attention and
+ * svdq_kv4_read may read keys and values from the same ones).
  * scale = e4m3_rne_satfinite(fp32(amax / 6)), code = e2m1_rne_satfinite(fp32(x / scale)),
  * as svdq_quantize_weight.
  */
@@ -110,7 +112,7 @@ SVDQ_API svdq_status svdq_kv4_read(const svdq_kv4_cache* cache, const svdq_heads
  * lse -inf.  Tokens before q_start[0] and from q_start[requests] on are left
  * as they were in out and lse.  Lengths are clamped to the table's capacity;
  * keys in a page outside [0, pages) do not exist.  q_start has to ascend.
- * q and out must not overlap.  Products are exact in fp32 per term, sums and
+ * out and lse must not overlap what is read.  Products are exact in fp32 per term, sums and
  * softmax fp32, softmax weights rounded to fp16 for the product with v (2^-11
  * of themselves, or 2^-32 of the row's largest where that is more).
  * max_kv_len: an upper bound of kv_len for scheduling (0: the table's

@@ -220,3 +220,17 @@ def test_every_size_of_a_call_is_planned(lib, requests, ragged):
     for tokens in range(requests, 1100, 1 if requests == 1 else requests):
         d = _attn(tokens=tokens, requests=requests, max_pages=4096, q_start=256 if ragged else None)
         assert lib.svdq_kv4_attention_workspace_bytes(ctypes.addressof(d)) > 0, tokens
+
+
+# ------------------------------------------------------------------ outputs that lie over inputs
+
+def test_overlap_of_strided_heads(tmp_path):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    exe = str(tmp_path / "head_overlap_check")
+    subprocess.run([cxx, "-O2", "-std=c++17", "-I", B.CSRC, os.path.join(ROOT, "tests", "native", "head_overlap_check.cpp"),
+                    "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout
+    assert r.stdout.strip() == "ok"

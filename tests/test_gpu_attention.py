@@ -824,3 +824,68 @@ def test_many_small_weights_beside_a_large_one(new, dim, dtype):
     assert (bound < 0.02 * want).all()                          # (a bound that would notice their absence)
     assert_rounded(out[:, 0], want.expand(new, dim), bound.expand(new, dim), dtype)
     assert ((lse.double() - l).abs() <= ds + keys * 2.0 ** -24 + 2.0 ** -22 * (1 + l.abs())).all()
+
+
+# ------------------------------------------------------------------ outputs that lie over inputs, in packed buffers
+
+def test_outputs_over_inputs_of_a_packed_buffer_are_refused():
+    q, cache, lens, table, start, causal = make(([64, 32], 2, 4, 2, 64, 16, True, BF), 131)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = S.kv4_attention(q, cache, n, table)
+    packed = torch.zeros(6, 12, 64, dtype=BF, device="cuda")
+    by_head = torch.zeros(12, 6, 64, dtype=BF, device="cuda").transpose(0, 1)
+    for buf in (packed, by_head):
+        buf[:4, :4] = q
+        for out in (buf[:4, 1:5], buf[:4, 3:7], buf[1:5, :4], buf[2:6, 2:6], buf[:4, 0:8:2], buf[1:5, 3:12:2][:, :4]):
+            with pytest.raises(ValueError, match="overlap"):
+                S.kv4_attention(buf[:4, :4], cache, n, table, out=out)
+        for out in (buf[:4, 4:8], buf[:4, 4:12:2]):
+            S.kv4_attention(buf[:4, :4], cache, n, table, out=out)
+            assert torch.equal(out, want) and torch.equal(buf[:4, :4], q)
+        buf.zero_()
+        buf[:4, 0:8:2] = q                                       # heads of queries and outputs in turn
+        S.kv4_attention(buf[:4, 0:8:2], cache, n, table, out=buf[:4, 1:9:2])
+        assert torch.equal(buf[:4, 1:9:2], want) and torch.equal(buf[:4, 0:8:2], q)
+        w = torch.ones(64, dtype=BF, device="cuda")
+        before = buf.clone()
+        for k in (buf[:, 3:5], buf[:, 2:8:2], buf[:, :4]):
+            with pytest.raises(ValueError, match="overlap"):
+                S.qk_norm_rope(buf[:, :4], k, w, inplace=True)
+        assert torch.equal(buf, before)
+        S.qk_norm_rope(buf[:, :4], buf[:, 4:6], w, w, inplace=True)
+
+
+def test_outputs_over_the_cache_and_the_cache_over_inputs_are_refused():
+    page, h, d = 16, 2, 64
+    rows = 4 * h * page
+    arena = torch.zeros(rows * (d + d // 8) + 4 * 2 * h * d * 2, dtype=torch.uint8, device="cuda")
+    sizes, cache, at = (d // 2, d // 16, d // 2, d // 16), [], 0
+    for n in sizes:
+        cache.append(arena[at:at + rows * n].view(4, h, page, n))
+        at += rows * n
+    k, v = (arena[at + i * 4 * h * d * 2:][:4 * h * d * 2].view(BF).view(4, h, d) for i in range(2))
+    k.copy_(heads(gen(132), 4, h, d, BF))
+    v.copy_(heads(gen(133), 4, h, d, BF))
+    slots = torch.tensor([0, 17, 40, 63], device="cuda")
+    S.kv4_append(cache, k, v, slots)                             # side by side in one buffer
+    other = S.kv4_cache(4, page, h, d)
+    S.kv4_append(other, k, v, slots)
+    assert all(torch.equal(a, b) for a, b in zip(cache, other)) and cache[0].any()
+    over = arena[at - 512:][:4 * h * d * 2].view(BF).view(4, h, d)
+    for call in (lambda: S.kv4_append(cache, over, v, slots), lambda: S.kv4_append(cache, k, over, slots),
+                 lambda: S.kv4_append(cache, k, v, cache[2].view(-1)[:32].view(torch.int64)),
+                 lambda: S.kv4_append((cache[0], cache[1], cache[0], cache[3]), k, v, slots),
+                 lambda: S.kv4_append((cache[0], cache[1], cache[2], cache[1]), k, v, slots)):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    n = torch.tensor([60], dtype=torch.int32, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    for out in (over, cache[0].view(-1)[:4 * h * d * 2].view(BF).view(4, h, d)):
+        with pytest.raises(ValueError, match="overlap"):
+            S.kv4_attention(k, cache, n, table, out=out)
+    assert all(torch.equal(a, b) for a, b in zip(cache, other))
+    # Reading is free to share: keys that serve as values too.
+    both = (cache[0], cache[1], cache[0], cache[1])
+    a, b = S.kv4_read(both, slots)
+    assert torch.equal(a, b)
+    assert torch.equal(S.kv4_attention(k, both, n, table, out=v), S.kv4_attention(k, both, n, table))
