@@ -8,7 +8,12 @@ rotary positions, the paged 4-bit key/value cache, and attention over it.
 
 Tensors of heads are (tokens, heads, head_dim), bf16 or fp16, with head_dim contiguous; slices of a
 packed projection output are passed as they lie.  Everything runs on the tensors' device, on
-``stream`` or that device's current stream.  Forward only, like the rest of the package.
+``stream`` or that device's current stream; a ``stream`` stands for ``with torch.cuda.stream(stream)``, so waits
+between streams, and keeping tensors alive until a stream is done with them, are left to the caller.
+
+Forward only, like the rest of the package: results of inputs that require grad are part of their graph, and a
+backward pass through them raises; in place, or with an ``out``, such inputs are refused outside torch.no_grad().
+What is written over (the cache, ``out``, heads in place) changes its version, as in torch's own in-place operations.
 """
 from __future__ import annotations
 

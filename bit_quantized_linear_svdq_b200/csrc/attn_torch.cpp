@@ -9,6 +9,8 @@
 // `stream` argument has been made current by then.
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
@@ -108,26 +110,50 @@ void distinct(const at::Tensor& t, const char* name) {
 }
 // The memory of an argument: a tensor of heads, a block table (rows of contiguous numbers), or a contiguous tensor.
 struct Memory {
-  svdq::HeadRuns runs;                          // bytes 0: none
+  svdq::HeadRuns runs;
+  long long end;                                // past its last byte; runs.at if it has none
   const char* name;
+  at::Tensor tensor;
   Memory() = default;
-  Memory(const at::Tensor& t, const char* n) : name(n) {
+  Memory(const at::Tensor& t, const char* n) : name(n), tensor(t) {
     const long long size = (long long)t.element_size(), at = (long long)reinterpret_cast<uintptr_t>(t.data_ptr());
+    const auto size_of = t.sizes(), stride = t.strides();
     if (t.numel() == 0)
       runs = {at, 0, 0, 1, 1, 0};
-    else if (t.dim() == 3)
-      runs = {at, t.stride(0) * size, t.stride(1) * size, t.size(0), t.size(1), t.size(2) * size};
-    else if (t.dim() == 2)
-      runs = {at, t.stride(0) * size, 0, t.size(0), 1, t.size(1) * size};
+    else if (size_of.size() == 3)
+      runs = {at, stride[0] * size, stride[1] * size, size_of[0], size_of[1], size_of[2] * size};
+    else if (size_of.size() == 2)
+      runs = {at, stride[0] * size, 0, size_of[0], 1, size_of[1] * size};
     else
       runs = {at, 0, 0, 1, 1, (long long)t.numel() * size};
+    end = svdq::end_of(runs);
   }
 };
 // Refuses an output that lies over another argument (views of one buffer side by side are fine).
 void apart(const Memory& t, const Memory& other) {
-  if (t.runs.bytes == 0 || other.runs.bytes == 0 || !svdq::runs_overlap(t.runs, other.runs)) return;
+  if (t.runs.at >= other.end || other.runs.at >= t.end || t.runs.bytes == 0 || other.runs.bytes == 0) return;
+  if (!svdq::runs_overlap(t.runs, other.runs)) return;
   raise(PyExc_ValueError, "%s and %s overlap in memory", t.name, other.name);
 }
+// What torch's own in-place operations do: who saved the tensor for a backward pass learns that it changed.
+void changed(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+bool tracked(const at::Tensor& t) { return t.requires_grad() && at::GradMode::is_enabled(); }
+// An output that is given, or an input written over, cannot be part of a graph.
+void not_tracked(const at::Tensor& t, const char* name) {
+  if (tracked(t))
+    raise(PyExc_RuntimeError, "%s: requires grad, and this operator has no backward pass (call it under torch.no_grad())", name);
+}
+// A new output of inputs that require grad is part of their graph; a backward pass through it raises.
+void no_backward(at::Tensor& y, const char* name, const torch::autograd::variable_list& inputs) {
+  if (!y.defined()) return;
+  torch::autograd::set_history(
+      y, std::shared_ptr<torch::autograd::Node>(
+             new torch::autograd::NotImplemented(name, torch::autograd::collect_next_edges(inputs)),
+             torch::autograd::deleteNode));
+}
+
 // A contiguous vector of n elements (n < 0: any number).
 const at::Tensor& vector(PyObject* o, const char* name, at::ScalarType type, int64_t n, int* device) {
   const at::Tensor& t = on_device(o, name, device);
@@ -246,8 +272,17 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else if (given(a[3])) {
       raise(PyExc_ValueError, "k_weight without k");
     }
-    if (given(a[2])) d.q_weight = vector(a[2], "q_weight", q.scalar_type(), d.head_dim, &device).data_ptr();
-    if (given(a[3])) d.k_weight = vector(a[3], "k_weight", q.scalar_type(), d.head_dim, &device).data_ptr();
+    bool in_graph = tracked(q) || (k && tracked(*k));
+    if (given(a[2])) {
+      const at::Tensor& w = vector(a[2], "q_weight", q.scalar_type(), d.head_dim, &device);
+      d.q_weight = w.data_ptr();
+      in_graph |= tracked(w);
+    }
+    if (given(a[3])) {
+      const at::Tensor& w = vector(a[3], "k_weight", q.scalar_type(), d.head_dim, &device);
+      d.k_weight = w.data_ptr();
+      in_graph |= tracked(w);
+    }
     d.eps = (float)number(a[4]);
     d.axes = 1;
     if (given(a[6])) {
@@ -264,6 +299,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const at::Tensor& f = vector(a[6], "inv_freq", at::kFloat, -1, &device);
       d.pairs = count(f.size(0), "inv_freq");
       d.inv_freq = static_cast<const float*>(f.data_ptr());
+      in_graph |= tracked(f);
       if (given(a[7]))
         d.pair_axis = static_cast<const unsigned char*>(vector(a[7], "pair_axis", at::kByte, d.pairs, &device).data_ptr());
     } else if (given(a[5]) || given(a[7])) {
@@ -278,11 +314,18 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         distinct(*k, "k");
         apart(Memory(q, "q"), Memory(*k, "k"));
       }
+      for (const int i : {0, 1, 2, 3, 6})
+        if (given(a[i])) not_tracked(tensor(a[i], ""), "inplace");
       d.q_out = d.q;
       d.k_out = d.k;
-      return answer(svdq_qk_norm_rope(&d, current_stream(device)), PyTuple_Pack(2, a[0], a[1]));
+      const svdq_status status = svdq_qk_norm_rope(&d, current_stream(device));
+      if (status == SVDQ_OK) {
+        changed(q);
+        if (k) changed(*k);
+      }
+      return answer(status, PyTuple_Pack(2, a[0], a[1]));
     }
-    const at::Tensor q_out = empty(q.sizes(), q, q.scalar_type());
+    at::Tensor q_out = empty(q.sizes(), q, q.scalar_type());
     d.q_out = contiguous_heads(q_out);
     at::Tensor k_out;
     if (k) {
@@ -290,6 +333,13 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       d.k_out = contiguous_heads(k_out);
     }
     const svdq_status status = svdq_qk_norm_rope(&d, current_stream(device));
+    if (in_graph) {
+      torch::autograd::variable_list inputs;
+      for (const int i : {0, 1, 2, 3, 6})
+        if (given(a[i])) inputs.push_back(tensor(a[i], ""));
+      no_backward(q_out, "qk_norm_rope", inputs);
+      no_backward(k_out, "qk_norm_rope", inputs);
+    }
     return answer(status, Py_BuildValue("NN", THPVariable_Wrap(q_out), k ? THPVariable_Wrap(k_out) : Py_NewRef(Py_None)));
   });
 }
@@ -314,9 +364,11 @@ PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       for (int j = 0; j < i; ++j) apart(cache[i], cache[j]);
     }
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
-    return answer(svdq_kv4_append(&c, &ka, &va, count(slots.size(0), "slots"), dtype,
-                                  static_cast<const long long*>(slots.data_ptr()), current_stream(device)),
-                  Py_NewRef(Py_None));
+    const svdq_status status = svdq_kv4_append(&c, &ka, &va, count(slots.size(0), "slots"), dtype,
+                                               static_cast<const long long*>(slots.data_ptr()), current_stream(device));
+    if (status == SVDQ_OK)
+      for (const Memory& m : cache) changed(m.tensor);
+    return answer(status, Py_NewRef(Py_None));
   });
 }
 
@@ -345,7 +397,7 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& q = on_device(a[0], "q", &device);
     d.dtype = type_code(q, "q");
     Memory cache[4];
-    d.cache = cache_of(a[1], &device, cache);
+    d.cache = cache_of(a[1], &device, given(a[8]) ? cache : nullptr);
     d.q = heads_of(q, "q");
     d.tokens = count(q.size(0), "q");
     d.q_heads = count(q.size(1), "q");
@@ -382,6 +434,8 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       need_shape(out, "out", q.size(0), q.size(1), q.size(2));
       d.out = heads_of(out, "out");
       distinct(out, "out");
+      not_tracked(out, "out");
+      not_tracked(q, "q");
       const Memory written(out, "out");
       apart(written, Memory(q, "q"));
       for (const Memory& m : cache) apart(written, m);
@@ -402,6 +456,12 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const size_t size = svdq_kv4_attention_workspace_bytes(&d);
     if (size) work = empty({(int64_t)size}, q, at::kByte);
     const svdq_status status = svdq_kv4_attention(&d, size ? work.data_ptr() : nullptr, size, current_stream(device));
+    if (given(a[8])) {
+      if (status == SVDQ_OK) changed(out);
+    } else if (tracked(q)) {
+      no_backward(out, "kv4_attention", {q});
+    }
+    if (want_lse && tracked(q)) no_backward(lse, "kv4_attention", {q});
     PyObject* first = given(a[8]) ? Py_NewRef(a[8]) : THPVariable_Wrap(out);
     return answer(status, want_lse ? Py_BuildValue("NN", first, THPVariable_Wrap(lse)) : first);
   });

@@ -53,11 +53,13 @@ inline HeadRuns merged(HeadRuns r) {
   return r;
 }
 
+inline long long end_of(const HeadRuns& r) {
+  return r.at + (r.tokens - 1) * r.token_stride + (r.heads - 1) * r.head_stride + r.bytes;
+}
+
 // (Strides of at least 0.)
 inline bool runs_overlap(HeadRuns a, HeadRuns b) {
-  const long long end_a = a.at + (a.tokens - 1) * a.token_stride + (a.heads - 1) * a.head_stride + a.bytes;
-  const long long end_b = b.at + (b.tokens - 1) * b.token_stride + (b.heads - 1) * b.head_stride + b.bytes;
-  if (a.at >= end_b || b.at >= end_a) return false;
+  if (a.at >= end_of(b) || b.at >= end_of(a)) return false;
   a = merged(a);
   b = merged(b);
   const long long c = a.at - b.at, lo = -a.bytes, hi = b.bytes;

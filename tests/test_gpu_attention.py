@@ -889,3 +889,80 @@ def test_outputs_over_the_cache_and_the_cache_over_inputs_are_refused():
     a, b = S.kv4_read(both, slots)
     assert torch.equal(a, b)
     assert torch.equal(S.kv4_attention(k, both, n, table, out=v), S.kv4_attention(k, both, n, table))
+
+
+# ------------------------------------------------------------------ autograd: no backward pass, and no silence about it
+
+def test_gradients_are_refused_not_lost():
+    q, cache, lens, table, _, _ = make(([64, 32], 2, 4, 2, 64, 16, True, BF), 141)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    w = torch.ones(64, dtype=BF, device="cuda")
+    f, _ = S.rope_frequencies((32,))
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")
+    k = heads(gen(142), 4, 2, 64, BF)
+
+    def norm(x=q, y=k, a=w, b=w, g=f, **kw):
+        return S.qk_norm_rope(x, y, a, b, positions=pos, inv_freq=g, **kw)
+
+    def grad(t):
+        return t.clone().requires_grad_()
+
+    def attend(x, **kw):
+        return S.kv4_attention(x, cache, n, table, return_lse=True, **kw)
+
+    plain, seen = norm(), attend(q)
+    assert not any(t.requires_grad for t in plain + seen)
+    for name, want, got in [("qk_norm_rope", plain, norm(x=grad(q))), ("qk_norm_rope", plain, norm(y=grad(k))),
+                            ("qk_norm_rope", plain, norm(a=grad(w))), ("qk_norm_rope", plain, norm(b=grad(w))),
+                            ("qk_norm_rope", plain, norm(g=grad(f))), ("kv4_attention", seen, attend(grad(q))),
+                            ("qk_norm_rope", plain, norm(x=grad(q) * 1.0, y=k.expand(4, 2, 64)))]:
+        for a, b in zip(want, got):
+            assert torch.equal(a, b) and b.requires_grad
+            with pytest.raises(RuntimeError, match=name + " is not implemented"):
+                b.float().sum().backward()
+    assert not S.qk_norm_rope(grad(q).detach())[0].requires_grad
+    with torch.no_grad():
+        assert not any(t.requires_grad for t in norm(x=grad(q)) + attend(grad(q)))
+    for call in (lambda: norm(x=grad(q), inplace=True), lambda: norm(x=q.clone(), y=grad(k), inplace=True),
+                 lambda: norm(x=q.clone(), y=k.clone(), a=grad(w), inplace=True),
+                 lambda: attend(q, out=grad(q)), lambda: attend(grad(q), out=torch.empty_like(q))):
+        with pytest.raises(RuntimeError, match="no backward pass"):
+            call()
+    with torch.no_grad():
+        x = grad(q)
+        assert torch.equal(norm(x=x, y=k.clone(), inplace=True)[0], plain[0])
+        out = torch.empty_like(q)
+        assert torch.equal(attend(grad(q), out=out)[0], seen[0])
+
+
+def test_written_tensors_change_their_version():
+    q, cache, lens, table, _, _ = make(([64, 32], 2, 4, 2, 64, 16, True, BF), 143)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    k = heads(gen(144), 4, 2, 64, BF)
+    out = torch.empty_like(q)
+
+    def versions():
+        return [t._version for t in (q, k, out, *cache)]
+
+    v = versions()
+    S.kv4_append(cache, k, k, torch.arange(4, device="cuda"))
+    assert versions() == v[:3] + [x + 1 for x in v[3:]]
+    v = versions()
+    S.kv4_attention(q, cache, n, table, out=out)
+    assert versions() == v[:2] + [v[2] + 1] + v[3:]
+    v = versions()
+    S.kv4_read(cache, torch.arange(4, device="cuda"))
+    S.qk_norm_rope(q, k)
+    assert versions() == v
+    w = torch.ones(4, 1, 1, device="cuda", dtype=BF, requires_grad=True)
+    y = (w * q).sum()                                            # keeps q for w's gradient
+    S.qk_norm_rope(q, k, inplace=True)
+    assert versions() == [v[0] + 1, v[1] + 1] + v[2:]
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        y.backward()
+    with torch.inference_mode():                                 # tensors that have no version
+        c, a = S.kv4_cache(4, 16, 2, 64), k.clone()
+        S.kv4_append(c, a, a, torch.arange(4, device="cuda"))
+        S.qk_norm_rope(a, inplace=True)
+    S.kv4_append(c, k, k, torch.arange(4, device="cuda"))
+    assert S.kv4_read(c, torch.arange(4, device="cuda"))[0].any()
