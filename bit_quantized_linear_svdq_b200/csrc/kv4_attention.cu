@@ -197,7 +197,7 @@ __device__ __forceinline__ void attend_segment(const Kv4AttnLaunch& p, const Row
     const int e = row_exponent(big);
     const float up = __uint_as_float((uint32_t)(127 + e) << 23);
     if (t == 0) {
-      back[8 * warp + g] = p.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
+      back[8 * warp + g] = row_factor(p.scale, e);
       sees[8 * warp + g] = q_sees;
     }
 #pragma unroll

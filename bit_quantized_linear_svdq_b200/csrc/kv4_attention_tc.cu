@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
                                   half2u(f[6] * up, f[7] * up)));
           // (Never zero: the mask writes -inf over scores, and -inf x 0 is no number.  At the smallest normal number what
           // is visible stays below 2^-90, as good as zero.)
-          const float down = fmaxf(sign * p.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23), 0x1p-126f);
+          const float down = fmaxf(row_factor(sign * p.scale, e), 0x1p-126f);
           const float theirs = __shfl_sync(0xFFFFFFFFu, down, (lane % kAtOnce) * kPieces);
           if (lane / kAtOnce == i) qs = theirs;             // row kAtOnce * i + lane % kAtOnce is this lane's
         }

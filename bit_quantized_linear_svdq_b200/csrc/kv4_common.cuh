@@ -4,6 +4,8 @@
 
 #include <cuda_runtime.h>
 
+#include <cfloat>
+
 #include "attn_kernels.h"
 #include "kcommon.cuh"
 #include "kv4_codes.cuh"
@@ -57,6 +59,13 @@ __device__ __forceinline__ void unpack8(uint4 w, float* v) {
 // Exponent e with 2^e * big in [2^14, 2^15), clamped so that 2^e and 2^-e are normal numbers.
 __device__ __forceinline__ int row_exponent(float big) {
   return big > 0.0f ? min(max(14 - (int)((__float_as_uint(big) >> 23) & 0xFF) + 127, -126), 126) : 0;
+}
+
+// Factor of a row's scores to exponents in base 2: its queries were scaled by 2^e.  Kept finite: a score of zero stays
+// zero whatever the scale.
+__device__ __forceinline__ float row_factor(float scale, int e) {
+  const float f = scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
+  return fminf(fmaxf(f, -FLT_MAX), FLT_MAX);
 }
 
 // A row's log sum from its reference and its sum of weights (not 0).  The room is taken out of both first: a log of

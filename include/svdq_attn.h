@@ -109,7 +109,9 @@ SVDQ_API svdq_status svdq_kv4_read(const svdq_kv4_cache* cache, const svdq_heads
  *   out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
  * Query head h reads key head h / (q_heads / heads).
  * A query without a key (kv_len 0, or causal with kv_len < n) gets out 0 and
- * lse -inf.  Tokens before q_start[0] and from q_start[requests] on are left
+ * lse -inf; one whose scores are all -inf (an infinite query) counts as such.
+ * softmax_scale may be any finite number, 0 and negative ones included; scores
+ * past fp32's range give NaN.  Tokens before q_start[0] and from q_start[requests] on are left
  * as they were in out and lse.  Lengths are clamped to the table's capacity;
  * keys in a page outside [0, pages) do not exist.  q_start has to ascend.
  * out and lse must not overlap what is read.  Products are exact in fp32 per term, sums and

@@ -966,3 +966,14 @@ def test_written_tensors_change_their_version():
         S.qk_norm_rope(a, inplace=True)
     S.kv4_append(c, k, k, torch.arange(4, device="cuda"))
     assert S.kv4_read(c, torch.arange(4, device="cuda"))[0].any()
+
+
+@pytest.mark.parametrize("new", [3, 150])
+def test_largest_scales(new):
+    """Scores of zero stay zero under any scale; tiny queries under a large one have scores of ordinary size."""
+    q, cache, lens, table, start, causal = make(([200], new, 2, 1, 128, 16, True, BF), 151)
+    top = float(torch.finfo(torch.float32).max)
+    for scale in (top, -top, 2.0 ** 127):
+        check(torch.zeros_like(q), cache, lens, table, None, True, scale=scale)
+    for scale in (1e36, -3e36):
+        check(q * 1e-37, cache, lens, table, None, True, scale=scale)
