@@ -977,3 +977,67 @@ def test_largest_scales(new):
         check(torch.zeros_like(q), cache, lens, table, None, True, scale=scale)
     for scale in (1e36, -3e36):
         check(q * 1e-37, cache, lens, table, None, True, scale=scale)
+
+
+# ------------------------------------------------------------------ every instance of the few-row kernel, and both kernels in one call
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [3, 8, 9, 16, 17, 23, 24, 25, 32, 33, 64, 65])
+def test_group_sizes(group, dim, dtype):
+    """Rows a request of each tile of the few-row kernel (8, 16, 24 and 32 rows), one past it, and past that kernel."""
+    q, cache, lens, table, start, causal = make(([300, 37], 1, 2 * group, 2, dim, 16, True, dtype), 161)
+    check(q, cache, lens, table, start, causal)
+    case = ([300, 37], [0, 3, 4], 2 * group, 2, dim, 32, True, dtype)
+    q, cache, lens, table, start, causal = make(case, 162)
+    check(q, cache, lens, table, start, causal)
+
+
+@pytest.mark.parametrize("dim,dtype,causal", [(128, BF, True), (128, FP, True), (64, BF, True), (128, BF, False)])
+def test_prompts_beside_single_and_drafted_tokens(dim, dtype, causal):
+    lens = [650, 1, 300, 129, 0, 280, 90, 33, 512]
+    start = [0, 1, 2, 180, 181, 182, 190, 191, 195, 400]
+    q, cache, lens, table, start, _ = make((lens, start, 8, 2, dim, 32, causal, dtype), 163)
+    a = check(q, cache, lens, table, start, causal)
+    b = check(q, cache, lens, table, start, causal)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1].nan_to_num(), b[1].nan_to_num())
+    check(q, cache, lens, table, start, causal, scale=-0.15, max_kv_len=700)
+
+
+# ------------------------------------------------------------------ the C entry points by their descriptions
+
+def test_calls_by_description():
+    """The ctypes mirrors of the header against the calls with tensors."""
+    t, hq, h, d, page = 5, 4, 2, 128, 16
+    g = gen(164)
+    packed = heads(g, t, hq + 2 * h, d, FP)
+    q, k, v = packed[:, :hq], packed[:, hq:hq + h], packed[:, hq + h:]
+    w = torch.rand(d, device="cuda", generator=g).to(FP)
+    f, axis = S.rope_frequencies((16, 24))
+    pos = torch.randint(0, 999, (t, 2), device="cuda", generator=g, dtype=torch.int32)
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def side(x):
+        return attention.svdq_heads(x.data_ptr(), x.stride(0), x.stride(1))
+
+    want = S.qk_norm_rope(q, k, w, w, positions=pos, inv_freq=f, pair_axis=axis, hadamard=True)
+    qo, ko = torch.empty(t, hq, d, dtype=FP, device="cuda"), torch.empty(t, h, d, dtype=FP, device="cuda")
+    attention.svdq_qk_norm_rope(attention.svdq_qk_norm_rope_desc(
+        t, hq, h, d, 1, side(q), side(k), side(qo), side(ko), w.data_ptr(), w.data_ptr(), 1e-6, pos.data_ptr(), 2, 2,
+        f.data_ptr(), axis.data_ptr(), 40, 0, 1), stream)
+    assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+    caches = [S.kv4_cache(3, page, h, d) for _ in range(2)]
+    slots = torch.tensor([40, 3, -1, 17, 16], device="cuda")
+    S.kv4_append(caches[0], ko, v, slots)
+    c = attention.svdq_kv4_cache(*(x.data_ptr() for x in caches[1]), 3, h, page, d)
+    attention.svdq_kv4_append(c, side(ko), side(v), t, 1, slots.data_ptr(), stream)
+    assert all(torch.equal(a, b) for a, b in zip(*caches)) and caches[1][0].any()
+    lens, table = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([9], [[1, 2]]))
+    want = S.kv4_attention(qo, caches[0], lens, table, return_lse=True)
+    out, lse = torch.empty_like(qo), torch.empty(t, hq, device="cuda")
+    desc = attention.svdq_kv4_attention_desc(c, t, 1, hq, 1, side(qo), side(out), lse.data_ptr(), lens.data_ptr(), None,
+                                             table.data_ptr(), 2, 2, 0, 1, d ** -0.5)
+    size = attention.svdq_kv4_attention_workspace_bytes(desc)
+    work = torch.empty(max(size, 16), dtype=torch.uint8, device="cuda")
+    attention.svdq_kv4_attention(desc, work.data_ptr(), size, stream)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
