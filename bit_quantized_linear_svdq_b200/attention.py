@@ -201,7 +201,8 @@ def kv4_cache(pages: int, page_size: int, heads: int, head_dim: int, device="cud
 def kv4_append(cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
     """Quantize k, v (tokens, heads, head_dim) into the cache: token t goes to slot ``slots[t]`` = page *
     page_size + offset (int64).  Slots outside the cache (-1 for padding) are skipped; the others must differ.  The
-    cache's four tensors, k, v and slots may share a buffer, but not memory."""
+    cache's four tensors, k, v and slots may share a buffer, but not memory.  Blocks of 16 values keep magnitudes
+    from about 0.1 to 2688 (include/svdq_attn.h says what happens outside)."""
     _run((_native or _calls()).kv4_append, "svdq_kv4_append", k, stream, cache, k, v, slots)
 
 

@@ -69,7 +69,7 @@ struct Kv4AttnLaunch {
   float scale;                    // softmax scale
   // Set by kv4_attention_plan:
   int num_sms;
-  int tile_rows;                  // rows of a tile: 8, 16, 32 or 256
+  int tile_rows;                  // rows of a tile: 8, 16, 24, 32 or 256
   int min_rows, max_rows;         // requests with fewer or more rows are left out
   long long segments;             // tiles x heads, at most
   int ctas, join;                 // CTAs that share the work; whether segments may be cut

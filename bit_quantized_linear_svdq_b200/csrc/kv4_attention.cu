@@ -36,14 +36,17 @@
 // weights change lanes (an 8x8 transpose, movmatrix).
 //
 // Bound: codes and scales are 9/16 byte a value, read once (HBM), through a ring
-// of cp.async copies per warp (no barrier between warps).  Above that lies the
-// instruction issue: about 620 warp instructions per 32 keys of one head (D =
-// 128, up to 8 rows) at 3.2 a clock, of which 256 convert and scale the 8192
-// values (cvt.e2m1x2 takes any byte of a register; the same from shifts and
-// logic is 2.2 times slower).  64 sequences of up to 8192 keys, 32 query and 8
-// key heads: 102 us, 4.4 TB/s; two of 131059 keys, 4 key heads: 40 us, 3.7 TB/s;
-// one of 1021 keys: 8.0 us, set-up and latencies.  16-key tiles: 128 us on the
-// first; five CTAs an SM, with spills, 129.
+// of cp.async copies per warp (no barrier between warps).  64 sequences of up to
+// 8192 keys, 32 query and 8 key heads: 102 us, 4.4 TB/s; two of 131059 keys, 4 key
+// heads: 40 us, 3.7 TB/s; one of 1021 keys: 8.3 us, set-up and latencies.  No unit
+// is full on the first (second): issue slots 62% (59), 2.2 (2.0) instructions a
+// clock, the ALU pipe 54% (51), DRAM 53% (46).  About 620 warp instructions per 32
+// keys of one head (D = 128, up to 8 rows), 256 of which convert and scale the 8192
+// values (cvt.e2m1x2 takes any byte of a register; the same from shifts and logic
+// is 2.2 times slower), run on 3.5 warps a scheduler that wait on their own results,
+// and 30% of the shared-memory wavefronts are bank conflicts of the code loads
+// (keys k and k + 4 of the first product, k and k + 2 of the second).  16-key
+// tiles: 128 us on the first case; five CTAs an SM, with spills, 129.
 //
 // Keys past L, pages outside the cache and everything masked for a row
 // contribute nothing, NaN included: such rows of the ring are zero-filled, scores

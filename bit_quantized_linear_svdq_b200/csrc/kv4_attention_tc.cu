@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attention_tc_kernel(const __
           }
         }
         // ---- weights, two to a column, over the last 64 columns of the scores: those of columns 64-127 first, whose
-        // scores are at hand and whose outputs can begin, then those of columns 0-63, read once more meanwhile
+        // outputs begin while those of columns 0-63 are formed
         const float minus = ref == -INFINITY ? 0.0f : -ref;
         const uint64_t qs2 = pk2(qs, qs), minus2 = pk2(minus, minus);
         uint64_t part[2] = {0, 0};

@@ -20,9 +20,9 @@
 // reciprocals and on index divisions as on its blocks), two in flight a thread.
 //
 // Bound: 2 + 9/16 bytes a value (HBM).  16411 tokens of 8 heads x 128, keys and
-// values, of 4 x 8 packed heads: 18.3 us to write (86 MB, 4.7 TB/s; the exact
-// division by the scale costs its issue slots), 14.8 us to read back (5.8
-// TB/s).  16-byte accesses instead of 32: 22 and 21 us; a grid of twice what is
+// values, of 4 x 8 packed heads: 18.3 us to write (86 MB, 4.7 TB/s; issue slots
+// 61%, the largest stall is the wait for loads), 14.8 us to read back (5.8 TB/s).
+// 16-byte accesses instead of 32: 22 and 21 us; a grid of twice what is
 // resident: 19.2 to write; one block in flight 19.4, four 21.8.
 #include <cuda_runtime.h>
 

@@ -42,7 +42,8 @@ typedef struct {
  * H is the Sylvester Hadamard of "Rotate in quantization and its vLLM
  * implementation" (section 3.2, per head_dim block): with it on queries and
  * keys alike q.k stays and keys lose less in 4 bits.
- * fp32 inside (the angle in fp64), one rounding to the storage type.
+ * fp32 inside (the angle in fp64), one rounding to the storage type; the sum of
+ * squares is fp32 too, so norms are for magnitudes below about 2^60.
  *   head_dim   multiple of 8, 8 .. 256; hadamard needs a power of two
  *   pairs      0 .. head_dim / 2; a multiple of 8 unless interleaved
  *   q_out/k_out may be q/k (in place); other overlaps are undefined
@@ -86,7 +87,11 @@ typedef struct {
  * cache's tensors may not overlap each other, k, v or slots here (attention and
  * svdq_kv4_read may read keys and values from the same ones).
  * scale = e4m3_rne_satfinite(fp32(amax / 6)), code = e2m1_rne_satfinite(fp32(x / scale)),
- * as svdq_quantize_weight.
+ * as svdq_quantize_weight.  There is no scale a tensor or head beside these: a
+ * block of 16 whose largest magnitude is at most 6 x 2^-10 (0.0059) becomes zeros,
+ * below 6 x 2^-6 (0.094) its scale has one to three bits, and magnitudes above
+ * 2688 saturate.  Values of another range are scaled by the caller, before the
+ * call and on attention's output.
  */
 SVDQ_API svdq_status svdq_kv4_append(const svdq_kv4_cache* cache, const svdq_heads* k, const svdq_heads* v,
                                      int tokens, int dtype, const long long* slots, void* stream);
