@@ -62,9 +62,9 @@ __device__ __forceinline__ int row_exponent(float big) {
 }
 
 // Factor of a row's scores to exponents in base 2: its queries were scaled by 2^e.  Kept finite: a score of zero stays
-// zero whatever the scale.
+// zero whatever the scale.  (Scale and log2 e alone may overflow where 2^-e brings their product back.)
 __device__ __forceinline__ float row_factor(float scale, int e) {
-  const float f = scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
+  const float f = scale * (kLog2e * __uint_as_float((uint32_t)(127 - e) << 23));
   return fminf(fmaxf(f, -FLT_MAX), FLT_MAX);
 }
 

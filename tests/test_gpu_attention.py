@@ -1041,3 +1041,10 @@ def test_calls_by_description():
     work = torch.empty(max(size, 16), dtype=torch.uint8, device="cuda")
     attention.svdq_kv4_attention(desc, work.data_ptr(), size, stream)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("new", [3, 150])
+def test_largest_scales_of_smallest_queries(new):
+    q, cache, lens, table, start, causal = make(([200], new, 2, 1, 128, 16, True, BF), 171)
+    for scale in (3e38, -3.4e38):
+        check(q * 1e-38, cache, lens, table, None, True, scale=scale)
