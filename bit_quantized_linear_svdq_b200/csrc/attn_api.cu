@@ -144,6 +144,7 @@ svdq_status svdq_qk_norm_rope(const svdq_qk_norm_rope_desc* d, void* stream) {
   if (!d) return fail(SVDQ_ERR_INVALID_ARG, "null description");
   if (d->tokens < 0 || (d->dtype != 0 && d->dtype != 1) || !(d->eps >= 0.0f))
     return fail(SVDQ_ERR_INVALID_ARG, "bad tokens, dtype or eps");
+  if (d->tokens > 0x7FFFFFFF - 4096) return fail(SVDQ_ERR_SHAPE, "too many tokens");     // (a CTA takes up to 4096)
   if (d->head_dim < 8 || d->head_dim > 256 || d->head_dim % 8 != 0)
     return fail(SVDQ_ERR_SHAPE, "head_dim has to be a multiple of 8, 8 .. 256");
   if (d->hadamard && (d->head_dim & (d->head_dim - 1)) != 0)

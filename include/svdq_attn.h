@@ -47,7 +47,7 @@ typedef struct {
  *   head_dim   multiple of 8, 8 .. 256; hadamard needs a power of two
  *   pairs      0 .. head_dim / 2; a multiple of 8 unless interleaved
  *   q_out/k_out may be q/k (in place); other overlaps are undefined
- *   strides    below 2^31 elements
+ *   strides    below 2^31 elements; tokens below 2^31 - 4096
  * tokens == 0 is a no-op; q_heads or k_heads may be 0.
  */
 typedef struct {

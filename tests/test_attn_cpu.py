@@ -234,3 +234,9 @@ def test_overlap_of_strided_heads(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout
     assert r.stdout.strip() == "ok"
+
+
+def test_more_tokens_than_the_grid_counts_are_refused(lib):
+    """The grid is ceil(tokens / tokens a CTA) in 32 bits, at most 4096 tokens a CTA."""
+    for tokens in (2 ** 31 - 1, 2 ** 31 - 4096):
+        assert lib.svdq_qk_norm_rope(ctypes.addressof(_rope(tokens=tokens, q_heads=1, k_heads=0, head_dim=8, pairs=0)), None) == 2
